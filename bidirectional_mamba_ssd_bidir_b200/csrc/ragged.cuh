@@ -1,0 +1,247 @@
+// ragged.cuh -- what the kernels on packed ragged batches share: where a sequence lies in the
+// packed rows, the state slots of a call, element types, and the launch interfaces of conv.cu,
+// step.cu, ragged.cu and ragged_tc.cu.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cstring>
+
+namespace ssd {
+
+// Codes that the kernels on packed batches write into the status word when an index array does not
+// hold what the call's contract says; the work concerned is skipped, nothing is read or written
+// outside the buffers.  (Codes below kArgCode are waits that gave up.)
+constexpr int kArgCode = 1000;
+constexpr int kCodeOffsets = 1001;    // cu_seqlens not ascending, or outside the packed rows
+constexpr int kCodeSlotRange = 1002;  // a slot index past the pool
+constexpr int kCodeSlotTwice = 1003;  // two sequences write the same slot
+
+// Sequences packed one after another: sequence i is rows [cu[i], cu[i+1]); cu == nullptr: each of
+// the nseq sequences has `len` rows.
+struct Packed {
+    const int *cu;
+    int nseq, tokens, len;
+};
+
+// The state slots of a call: sequence i starts from slot in[i] of pool_in (a negative index or no
+// pool: from zero) and leaves its last state in slot out[i] of pool_out (negative: not stored).
+// in/out == nullptr: slot i.
+struct Slots {
+    const void *pool_in;
+    void *pool_out;
+    const int *in, *out;
+    int n_in, n_out;
+};
+
+struct ConvArgs {
+    Packed seq;
+    Slots slots;
+    const void *x, *gy;
+    void *y;                       // y, or gx in the backward pass
+    long long ldx, ldy, ldg;       // row strides in elements
+    const float *w, *bias;         // [C][K]; bias may be null
+    int C, K, dir, silu;
+    int run, units, cblocks;       // tokens a CTA walks, CTAs along the packed rows and along the channels
+    int *status;                   // may be null
+    float *part, *gw, *gb;         // backward: partial sums [units][K + 1][C]; gb may be null
+};
+cudaError_t launch_conv(ConvArgs a, bool bf16, cudaStream_t st);
+cudaError_t launch_conv_bwd(ConvArgs a, bool bf16, cudaStream_t st);
+size_t conv_bwd_partial_floats(long long tokens, int C, int K);
+
+struct StepArgs {
+    int rows, H, P, N, G, C, K;    // C = H P + 2 G N channels
+    const void *xBC, *dt;
+    long long ldx, lddt, ldy;
+    const float *conv_w, *conv_b, *dt_bias, *A, *D;
+    void *conv_state;              // [n_slots][K - 1][C]
+    float *ssm_state;              // [n_slots][H][P][N]
+    const int *slots;
+    int n_slots;
+    float *v;                      // [rows][C + 4]: the convolution's outputs, then the row's slot (or -1)
+    void *y;
+    int *status;
+};
+cudaError_t launch_step(const StepArgs &a, bool bf16, cudaStream_t st);
+
+struct RaggedArgs {
+    Packed seq;
+    Slots slots;                   // float32 pools [n][H][P][N]
+    const void *x, *dt, *B, *C;
+    long long ldx, lddt, ldB, ldC, ldy;
+    const float *A, *D, *dt_bias;  // D, dt_bias may be null
+    void *y;
+    int H, P, N, G, dir;
+    int seg, units;                // tokens of a segment, segments at most
+    float *ws_state, *ws_decay;    // [units][H][P][N] and [units][H]
+    int *status;
+    long long wait_cycles;
+};
+// Segment length for a call: whole tiles of `quant` tokens, as few as give about `ctas` CTAs.
+inline int ragged_segment(long long tokens, long long ctas_per_segment, int quant, long long ctas) {
+    long long s = (tokens * ctas_per_segment + ctas - 1) / ctas;
+    s = (s + quant - 1) / quant * quant;
+    return (int)(s < quant ? quant : s);
+}
+cudaError_t launch_ragged_simt(const RaggedArgs &a, bool bf16, cudaStream_t st);
+
+#ifdef __CUDACC__
+namespace {
+
+__device__ __forceinline__ int seq_start(const Packed &s, int i) {
+    if (!s.cu) return i * s.len;
+    const int v = s.cu[i];
+    return v < 0 ? 0 : (v > s.tokens ? s.tokens : v);
+}
+
+// The last sequence that starts at or before row t (-1: none).
+__device__ __forceinline__ int seq_find(const Packed &s, int t) {
+    if (!s.cu) return s.len > 0 ? min(t / s.len, s.nseq - 1) : -1;
+    int lo = -1, hi = s.nseq;                 // start(lo) <= t < start(hi)
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (seq_start(s, m) <= t) lo = m;
+        else hi = m;
+    }
+    return lo;
+}
+
+// Segment u of a call (ragged.cu): its sequence s (-1: none), which of the sequence's `count`
+// segments it is, and the sequence's first row and length.  An empty sequence has one, empty, segment.
+struct Segment {
+    int s, k, count, lo, len;
+};
+__device__ __forceinline__ Segment find_segment(const Packed &q, int seg, int u) {
+    int lo = -1, hi = q.nseq;                 // start(lo) / seg + lo <= u < start(hi) / seg + hi
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (seq_start(q, m) / seg + m <= u) lo = m;
+        else hi = m;
+    }
+    Segment r{-1, 0, 0, 0, 0};
+    if (lo < 0) return r;
+    r.lo = seq_start(q, lo);
+    r.len = max(0, seq_start(q, lo + 1) - r.lo);
+    r.k = u - (r.lo / seg + lo);
+    r.count = max(1, (r.len + seg - 1) / seg);
+    r.s = r.k < r.count ? lo : -1;
+    return r;
+}
+
+__device__ __forceinline__ void report(int *status, int code) {
+    if (status) atomicCAS(status, 0, code);
+}
+
+// One CTA's look over cu_seqlens.
+__device__ __forceinline__ void check_offsets(const Packed &s, int *status) {
+    if (!s.cu || !status) return;
+    bool bad = false;
+    for (int i = threadIdx.x; i < s.nseq; i += blockDim.x)
+        bad |= s.cu[i] < 0 || s.cu[i + 1] < s.cu[i] || s.cu[i + 1] > s.tokens;
+    if (bad) report(status, kCodeOffsets);
+}
+
+// Slot that sequence i starts from (-1: zero state).
+__device__ __forceinline__ int slot_of_start(const Slots &s, int i, int *status) {
+    if (!s.pool_in) return -1;
+    const int v = s.in ? s.in[i] : i;
+    if (v >= s.n_in) {
+        report(status, kCodeSlotRange);
+        return -1;
+    }
+    return v < 0 ? -1 : v;
+}
+// Slot that sequence i ends in (-1: not stored).  Called by every thread of the CTA: a slot that a
+// second sequence names too is stored by neither.
+__device__ __forceinline__ int slot_of_end(const Slots &s, int i, int nseq, int *status) {
+    if (!s.pool_out) return -1;
+    const int v = s.out ? s.out[i] : i;
+    if (v < 0) return -1;
+    if (v >= s.n_out) {
+        report(status, kCodeSlotRange);
+        return -1;
+    }
+    if (!s.out) return v;
+    bool twice = false;
+    for (int j = threadIdx.x; j < nseq; j += blockDim.x) twice |= j != i && s.out[j] == v;
+    if (__syncthreads_or(twice)) {
+        report(status, kCodeSlotTwice);
+        return -1;
+    }
+    return v;
+}
+
+// V consecutive elements as float32, and back (rounded to nearest even)
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+template <typename T, int V> struct Vec;
+template <> struct Vec<__nv_bfloat16, 4> { using type = uint2; };
+template <> struct Vec<float, 4> { using type = uint4; };
+template <> struct Vec<__nv_bfloat16, 1> { using type = __nv_bfloat16; };
+template <> struct Vec<float, 1> { using type = float; };
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const typename Vec<T, V>::type &r, float (&f)[V]) {
+    T e[V];
+    memcpy(e, &r, sizeof(r));
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = to_f<T>(e[i]);
+}
+template <typename T, int V>
+__device__ __forceinline__ typename Vec<T, V>::type pack(const float (&f)[V]) {
+    T e[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) e[i] = from_f<T>(f[i]);
+    typename Vec<T, V>::type r;
+    memcpy(&r, e, sizeof(r));
+    return r;
+}
+
+__device__ __forceinline__ float softplus(float v) { return v > 20.f ? v : log1pf(expf(v)); }
+
+__device__ __forceinline__ float ex2a(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcpa(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// sigma[i] = 1 / (1 + e^-v[i]).  With e = e^-|v| <= 1 it is 1 / (1 + e) or e / (1 + e), which keeps
+// its relative accuracy on both sides and stays finite; the V divisions share one reciprocal, of the
+// product of the denominators (each within [1, 2], at most 16).  The denominator of a NaN counts as
+// 2, so it spoils its own channel alone.
+template <int V> __device__ __forceinline__ void sigmoids(const float (&v)[V], float (&sg)[V]) {
+    float e[V], d[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        e[i] = ex2a(-1.4426950408889634f * fabsf(v[i]));
+        d[i] = 1.f + fminf(e[i], 1.f);
+    }
+    if constexpr (V == 4) {
+        const float p01 = d[0] * d[1], p23 = d[2] * d[3], r = rcpa(p01 * p23);
+        const float r01 = r * p23, r23 = r * p01;
+        const float inv[4] = {r01 * d[1], r01 * d[0], r23 * d[3], r23 * d[2]};
+#pragma unroll
+        for (int i = 0; i < V; ++i) sg[i] = (v[i] >= 0.f ? 1.f : e[i]) * inv[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) sg[i] = (v[i] >= 0.f ? 1.f : e[i]) * rcpa(d[i]);
+    }
+}
+
+}  // namespace
+#endif
+
+}  // namespace ssd

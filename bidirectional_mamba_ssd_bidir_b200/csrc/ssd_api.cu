@@ -9,6 +9,7 @@
 #include "../../include/bidir_ssd.h"
 #include "attention.cuh"
 #include "mixer.cuh"
+#include "ragged.cuh"
 #include "ssd_internal.cuh"
 #include "ssd_tc.cuh"
 
@@ -375,6 +376,11 @@ ssd_status ssd_workspace_status(void *workspace, size_t workspace_bytes, void *s
         e = cudaMemsetAsync(workspace, 0, sizeof(int), cs);
         if (e == cudaSuccess) e = cudaStreamSynchronize(cs);
         if (e != cudaSuccess) return cuda_fail(e, "status clear");
+        switch (word) {
+            case ssd::kCodeOffsets: return fail(SSD_ERR_INVALID_ARG, "cu_seqlens not ascending, or outside the packed rows");
+            case ssd::kCodeSlotRange: return fail(SSD_ERR_INVALID_ARG, "a slot index past the state pool");
+            case ssd::kCodeSlotTwice: return fail(SSD_ERR_INVALID_ARG, "two sequences or rows write one state slot");
+        }
         return fail(SSD_ERR_TIMEOUT, "a bounded device wait gave up (code %d)", word);
     }
     return SSD_OK;
@@ -676,6 +682,262 @@ ssd_status attention_block(const ssd_attn_shape *shape, int d_model, const void 
     if ((e = ssd::launch_gemm_bf16(g2, cs)) != cudaSuccess) return cuda_fail(e, "output projection");
     g_err.clear();
     return SSD_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- packed ragged batches and single tokens
+
+namespace {
+
+bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+size_t io_bytes(ssd_dtype io) { return io == SSD_BF16 ? 2 : 4; }
+
+ssd_status check_packed(const ssd_packed *q, ssd::Packed *out) {
+    if (!q) return fail(SSD_ERR_INVALID_ARG, "packed is NULL");
+    if (q->tokens < 0 || q->nseq < 0) return fail(SSD_ERR_INVALID_ARG, "negative token or sequence count");
+    if (q->nseq == 0 && q->tokens > 0 && !q->cu_seqlens) return fail(SSD_ERR_INVALID_ARG, "tokens in no sequence");
+    if (!q->cu_seqlens && q->nseq > 0 && q->tokens % q->nseq != 0)
+        return fail(SSD_ERR_INVALID_ARG, "%d tokens do not divide into %d equal sequences", q->tokens, q->nseq);
+    if (!aligned(q->cu_seqlens, 4)) return fail(SSD_ERR_INVALID_ARG, "cu_seqlens must be 4-byte aligned");
+    // room for the unit numbers of the kernels (tokens / segment + nseq)
+    if ((long long)q->tokens + q->nseq > 0x7fff0000LL) return fail(SSD_ERR_UNSUPPORTED, "too many tokens or sequences");
+    out->cu = q->cu_seqlens;
+    out->nseq = q->nseq;
+    out->tokens = q->tokens;
+    out->len = q->nseq > 0 ? q->tokens / q->nseq : 0;
+    return SSD_OK;
+}
+
+ssd_status check_slots(const ssd_slots *q, int nseq, size_t align, ssd::Slots *out) {
+    *out = ssd::Slots{};
+    if (!q) return SSD_OK;
+    if (!aligned(q->pool_in, align) || !aligned(q->pool_out, align) || !aligned(q->slots_in, 4) || !aligned(q->slots_out, 4))
+        return fail(SSD_ERR_INVALID_ARG, "state pools and slots must be aligned to their element");
+    if (q->n_in < 0 || q->n_out < 0) return fail(SSD_ERR_INVALID_ARG, "negative slot count");
+    if ((q->pool_in && !q->slots_in && q->n_in < nseq) || (q->pool_out && !q->slots_out && q->n_out < nseq))
+        return fail(SSD_ERR_INVALID_ARG, "a state pool without slot indices needs one slot per sequence (%d)", nseq);
+    out->pool_in = q->pool_in; out->pool_out = q->pool_out;
+    out->in = q->slots_in; out->out = q->slots_out;
+    out->n_in = q->n_in; out->n_out = q->n_out;
+    return SSD_OK;
+}
+
+// the optional status area of the calls that need no other workspace
+ssd_status check_status_area(void *ws, size_t bytes) {
+    if (ws && (!aligned(ws, 4) || bytes < kStatusBytes)) return fail(SSD_ERR_INVALID_ARG, "workspace of 256 bytes needed");
+    return SSD_OK;
+}
+
+ssd_status conv_args(const ssd_conv_shape *s, const ssd_packed *seq, ssd::ConvArgs *a) {
+    if (!s) return fail(SSD_ERR_INVALID_ARG, "shape is NULL");
+    if (s->io != SSD_BF16 && s->io != SSD_F32) return fail(SSD_ERR_INVALID_ARG, "unknown io dtype %d", (int)s->io);
+    if (s->channels <= 0) return fail(SSD_ERR_INVALID_ARG, "channels must be positive");
+    if (s->channels > (1 << 24)) return fail(SSD_ERR_UNSUPPORTED, "at most 2^24 channels");
+    if (s->width < 1 || s->width > 8) return fail(SSD_ERR_UNSUPPORTED, "convolution width %d not in 1..8", s->width);
+    if (s->direction != 1 && s->direction != -1) return fail(SSD_ERR_INVALID_ARG, "direction must be +1 or -1");
+    *a = ssd::ConvArgs{};
+    a->C = s->channels; a->K = s->width; a->dir = s->direction; a->silu = s->silu != 0;
+    return check_packed(seq, &a->seq);
+}
+
+ssd_status check_rows(const void *p, long long ld, long long width, size_t es, const char *what) {
+    if (!p || !aligned(p, es)) return fail(SSD_ERR_INVALID_ARG, "%s must be non-NULL and aligned to its element", what);
+    if (ld < width) return fail(SSD_ERR_INVALID_ARG, "%s: row stride %lld < %lld", what, ld, width);
+    return SSD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ssd_status ssd_conv(const ssd_conv_shape *shape, const ssd_packed *seq, const void *x, long long ldx, const float *w,
+                    const float *bias, const ssd_slots *state, void *y, long long ldy, void *workspace,
+                    size_t workspace_bytes, void *stream) {
+    g_err.clear();
+    ssd::ConvArgs a;
+    ssd_status st = conv_args(shape, seq, &a);
+    if (st != SSD_OK || (st = check_slots(state, a.seq.nseq, io_bytes(shape->io), &a.slots)) != SSD_OK) return st;
+    if ((st = check_status_area(workspace, workspace_bytes)) != SSD_OK) return st;
+    if (a.seq.nseq == 0) return SSD_OK;
+    const size_t es = io_bytes(shape->io);
+    if (a.seq.tokens > 0 && ((st = check_rows(x, ldx, a.C, es, "x")) != SSD_OK || (st = check_rows(y, ldy, a.C, es, "y")) != SSD_OK))
+        return st;
+    if (!w || !aligned(w, 4) || !aligned(bias, 4)) return fail(SSD_ERR_INVALID_ARG, "w must be non-NULL, w and bias 4-byte aligned");
+    a.x = x; a.ldx = ldx; a.w = w; a.bias = bias; a.y = y; a.ldy = ldy;
+    a.status = static_cast<int *>(workspace);
+    cudaError_t e = ssd::launch_conv(a, shape->io == SSD_BF16, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SSD_OK : cuda_fail(e, "convolution launch");
+}
+
+size_t ssd_conv_bwd_workspace_bytes(const ssd_conv_shape *shape, int tokens) {
+    ssd::ConvArgs a;
+    const ssd_packed one{nullptr, 1, tokens};
+    if (conv_args(shape, &one, &a) != SSD_OK) return 0;
+    return kStatusBytes + round_up(ssd::conv_bwd_partial_floats(tokens, a.C, a.K) * sizeof(float));
+}
+
+ssd_status ssd_conv_bwd(const ssd_conv_shape *shape, const ssd_packed *seq, const void *x, long long ldx, const float *w,
+                        const float *bias, const void *gy, long long ldg, void *gx, long long ldgx, float *gw, float *gb,
+                        void *workspace, size_t workspace_bytes, void *stream) {
+    g_err.clear();
+    ssd::ConvArgs a;
+    ssd_status st = conv_args(shape, seq, &a);
+    if (st != SSD_OK) return st;
+    if (!w || !gw || !aligned(w, 4) || !aligned(bias, 4) || !aligned(gw, 4) || !aligned(gb, 4))
+        return fail(SSD_ERR_INVALID_ARG, "w and gw must be non-NULL, w, bias, gw and gb 4-byte aligned");
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (a.seq.tokens == 0 || a.seq.nseq == 0) {
+        cudaError_t e = cudaMemsetAsync(gw, 0, sizeof(float) * a.C * a.K, cs);
+        if (e == cudaSuccess && gb) e = cudaMemsetAsync(gb, 0, sizeof(float) * a.C, cs);
+        return e == cudaSuccess ? SSD_OK : cuda_fail(e, "empty gradient clear");
+    }
+    const size_t es = io_bytes(shape->io);
+    if ((st = check_rows(x, ldx, a.C, es, "x")) != SSD_OK || (st = check_rows(gy, ldg, a.C, es, "gy")) != SSD_OK ||
+        (st = check_rows(gx, ldgx, a.C, es, "gx")) != SSD_OK)
+        return st;
+    const size_t need = ssd_conv_bwd_workspace_bytes(shape, a.seq.tokens);
+    if (!workspace || !aligned(workspace, kAlign)) return fail(SSD_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
+    if (workspace_bytes < need) return fail(SSD_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    a.x = x; a.ldx = ldx; a.w = w; a.bias = bias; a.gy = gy; a.ldg = ldg; a.y = gx; a.ldy = ldgx; a.gw = gw; a.gb = gb;
+    a.status = static_cast<int *>(workspace);
+    a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + kStatusBytes);
+    cudaError_t e = ssd::launch_conv_bwd(a, shape->io == SSD_BF16, cs);
+    return e == cudaSuccess ? SSD_OK : cuda_fail(e, "convolution gradient launch");
+}
+
+}  // extern "C"
+
+namespace {
+
+ssd_status check_heads(int H, int P, int N, int G, ssd_dtype io) {
+    if (H <= 0 || P <= 0 || N <= 0 || G <= 0) return fail(SSD_ERR_INVALID_ARG, "negative or zero size in shape");
+    if (io != SSD_BF16 && io != SSD_F32) return fail(SSD_ERR_INVALID_ARG, "unknown io dtype %d", (int)io);
+    static const int P_ok[] = {16, 32, 64}, N_ok[] = {16, 32, 64, 128};
+    if (!is_pow2_in(P, P_ok, 3)) return fail(SSD_ERR_UNSUPPORTED, "headdim %d not in {16,32,64}", P);
+    if (!is_pow2_in(N, N_ok, 4)) return fail(SSD_ERR_UNSUPPORTED, "dstate %d not in {16,32,64,128}", N);
+    if (H % G != 0) return fail(SSD_ERR_UNSUPPORTED, "nheads %d not a multiple of ngroups %d", H, G);
+    if (H > 65535 / 4) return fail(SSD_ERR_UNSUPPORTED, "at most 16383 heads");
+    return SSD_OK;
+}
+
+size_t step_ws_bytes(const ssd_step_shape *s) {
+    const size_t C = (size_t)s->nheads * s->headdim + 2 * (size_t)s->ngroups * s->dstate;
+    return kStatusBytes + round_up((size_t)s->rows * (C + 4) * sizeof(float));
+}
+
+ssd_status check_step(const ssd_step_shape *s) {
+    if (!s) return fail(SSD_ERR_INVALID_ARG, "shape is NULL");
+    if (s->rows < 0 || s->n_slots < 0) return fail(SSD_ERR_INVALID_ARG, "negative row or slot count");
+    if (s->rows > 65535) return fail(SSD_ERR_UNSUPPORTED, "at most 65535 rows");
+    if (s->d_conv < 1 || s->d_conv > 8) return fail(SSD_ERR_UNSUPPORTED, "convolution width %d not in 1..8", s->d_conv);
+    return check_heads(s->nheads, s->headdim, s->dstate, s->ngroups, s->io);
+}
+
+struct RaggedPlan {
+    int seg, units;
+    size_t state, decay, total;     // workspace offsets and size
+};
+
+ssd_status ragged_plan(const ssd_ragged_shape *s, long long tokens, int nseq, RaggedPlan *p) {
+    if (!s) return fail(SSD_ERR_INVALID_ARG, "shape is NULL");
+    ssd_status st = check_heads(s->nheads, s->headdim, s->dstate, s->ngroups, s->io);
+    if (st != SSD_OK) return st;
+    if (tokens < 0 || nseq < 0 || tokens + nseq > 0x7fff0000LL) return fail(SSD_ERR_INVALID_ARG, "bad token or sequence count");
+    // segments for about four CTAs per SM
+    p->seg = ssd::ragged_segment(tokens, s->nheads, 64, 4 * 148);
+    p->units = (int)(tokens / p->seg) + nseq;
+    // sequences no longer than a segment need no states between launches
+    const size_t n = tokens > p->seg ? (size_t)p->units * s->nheads : 0;
+    p->state = kStatusBytes;
+    p->decay = p->state + round_up(n * s->headdim * s->dstate * sizeof(float));
+    p->total = p->decay + round_up(n * sizeof(float));
+    return SSD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssd_step_workspace_bytes(const ssd_step_shape *shape) {
+    return check_step(shape) == SSD_OK ? step_ws_bytes(shape) : 0;
+}
+
+ssd_status mamba2_step(const ssd_step_shape *shape, const void *xBC, long long ldx, const void *dt, long long lddt,
+                       const float *conv_w, const float *conv_b, const float *dt_bias, const float *A, const float *D,
+                       void *conv_state, float *ssm_state, const int *slots, void *y, long long ldy, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    g_err.clear();
+    ssd_status st = check_step(shape);
+    if (st != SSD_OK) return st;
+    if (shape->rows == 0) return SSD_OK;
+    const size_t es = io_bytes(shape->io);
+    const int di = shape->nheads * shape->headdim, C = di + 2 * shape->ngroups * shape->dstate;
+    if ((st = check_rows(xBC, ldx, C, es, "xBC")) != SSD_OK || (st = check_rows(dt, lddt, shape->nheads, es, "dt")) != SSD_OK ||
+        (st = check_rows(y, ldy, di, es, "y")) != SSD_OK)
+        return st;
+    if (!conv_w || !A || !aligned(conv_w, 4) || !aligned(conv_b, 4) || !aligned(dt_bias, 4) || !aligned(A, 4) || !aligned(D, 4))
+        return fail(SSD_ERR_INVALID_ARG, "conv_w and A must be non-NULL, float32 arrays 4-byte aligned");
+    if ((!conv_state && shape->d_conv > 1) || !aligned(conv_state, es) || !aligned16(ssm_state))
+        return fail(SSD_ERR_INVALID_ARG, "the states must be non-NULL, ssm_state 16-byte aligned");
+    if (!aligned(slots, 4)) return fail(SSD_ERR_INVALID_ARG, "slots must be 4-byte aligned");
+    if (shape->n_slots < 1 || (!slots && shape->n_slots < shape->rows))
+        return fail(SSD_ERR_INVALID_ARG, "%d slots for %d rows", shape->n_slots, shape->rows);
+    const size_t need = step_ws_bytes(shape);
+    if (!workspace || !aligned(workspace, kAlign)) return fail(SSD_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
+    if (workspace_bytes < need) return fail(SSD_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    ssd::StepArgs a{};
+    a.rows = shape->rows; a.H = shape->nheads; a.P = shape->headdim; a.N = shape->dstate; a.G = shape->ngroups;
+    a.C = C; a.K = shape->d_conv;
+    a.xBC = xBC; a.ldx = ldx; a.dt = dt; a.lddt = lddt; a.conv_w = conv_w; a.conv_b = conv_b; a.dt_bias = dt_bias;
+    a.A = A; a.D = D; a.conv_state = conv_state; a.ssm_state = ssm_state; a.slots = slots; a.n_slots = shape->n_slots;
+    a.y = y; a.ldy = ldy;
+    a.status = static_cast<int *>(workspace);
+    a.v = reinterpret_cast<float *>(static_cast<char *>(workspace) + kStatusBytes);
+    cudaError_t e = ssd::launch_step(a, shape->io == SSD_BF16, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SSD_OK : cuda_fail(e, "step launch");
+}
+
+size_t ssd_ragged_workspace_bytes(const ssd_ragged_shape *shape, int tokens, int nseq) {
+    RaggedPlan p;
+    return ragged_plan(shape, tokens, nseq, &p) == SSD_OK ? p.total : 0;
+}
+
+ssd_status ssd_scan_ragged(const ssd_ragged_shape *shape, const ssd_packed *seq, const ssd_ragged_params *p, int direction,
+                           const ssd_slots *state, void *y, long long ldy, void *workspace, size_t workspace_bytes,
+                           void *stream) {
+    g_err.clear();
+    ssd::RaggedArgs a{};
+    RaggedPlan plan;
+    ssd_status st = check_packed(seq, &a.seq);
+    if (st != SSD_OK || (st = ragged_plan(shape, a.seq.tokens, a.seq.nseq, &plan)) != SSD_OK) return st;
+    if (direction != 1 && direction != -1) return fail(SSD_ERR_INVALID_ARG, "direction must be +1 or -1");
+    if ((st = check_slots(state, a.seq.nseq, 4, &a.slots)) != SSD_OK) return st;
+    if (!p) return fail(SSD_ERR_INVALID_ARG, "params is NULL");
+    if (a.seq.nseq == 0) return SSD_OK;
+    const size_t es = io_bytes(shape->io);
+    const int HP = shape->nheads * shape->headdim, GN = shape->ngroups * shape->dstate;
+    if (a.seq.tokens > 0 &&
+        ((st = check_rows(p->x, p->ldx, HP, es, "x")) != SSD_OK || (st = check_rows(p->dt, p->lddt, shape->nheads, es, "dt")) != SSD_OK ||
+         (st = check_rows(p->B, p->ldB, GN, es, "B")) != SSD_OK || (st = check_rows(p->C, p->ldC, GN, es, "C")) != SSD_OK ||
+         (st = check_rows(y, ldy, HP, es, "y")) != SSD_OK))
+        return st;
+    if (!p->A || !aligned(p->A, 4) || !aligned(p->D, 4) || !aligned(p->dt_bias, 4))
+        return fail(SSD_ERR_INVALID_ARG, "A must be non-NULL, A, D and dt_bias 4-byte aligned");
+    if (!workspace || !aligned(workspace, kAlign)) return fail(SSD_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
+    if (workspace_bytes < plan.total) return fail(SSD_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed", workspace_bytes, plan.total);
+    a.x = p->x; a.dt = p->dt; a.B = p->B; a.C = p->C;
+    a.ldx = p->ldx; a.lddt = p->lddt; a.ldB = p->ldB; a.ldC = p->ldC;
+    a.A = p->A; a.D = p->D; a.dt_bias = p->dt_bias; a.y = y; a.ldy = ldy;
+    a.H = shape->nheads; a.P = shape->headdim; a.N = shape->dstate; a.G = shape->ngroups; a.dir = direction;
+    a.seg = plan.seg; a.units = plan.units;
+    char *ws = static_cast<char *>(workspace);
+    a.ws_state = reinterpret_cast<float *>(ws + plan.state);
+    a.ws_decay = reinterpret_cast<float *>(ws + plan.decay);
+    a.status = static_cast<int *>(workspace);
+    a.wait_cycles = wait_cycles_now();
+    cudaError_t e = ssd::launch_ragged_simt(a, shape->io == SSD_BF16, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SSD_OK : cuda_fail(e, "ragged scan launch");
 }
 
 }  // extern "C"

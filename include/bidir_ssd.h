@@ -333,6 +333,125 @@ size_t ssd_attention_block_workspace_bytes(const ssd_attn_shape *shape);
 ssd_status attention_block(const ssd_attn_shape *shape, int d_model, const void *u, const void *W_qkv,
                            const void *W_o, void *out, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The Mamba-2 layer on packed ragged batches, and one token at a time.
+ *
+ * The calls above take equal sequences of whole chunks.  Block-wise decoding
+ * (the DiffuMamba page, technical summary, section 2: block diffusion with
+ * cache reuse; section 4, block caching) continues prompts of any length from
+ * cached states, many at once, and then single tokens.
+ * ------------------------------------------------------------------------ */
+
+/* Sequences packed one behind another along the rows ("tokens") of every
+ * tensor: sequence i is rows [cu_seqlens[i], cu_seqlens[i+1]); cu_seqlens is a
+ * DEVICE array of nseq + 1 ints, ascending (equal neighbours: an empty
+ * sequence), within [0, tokens].  NULL: nseq sequences of tokens / nseq rows.
+ * Rows in no sequence (a padded batch's tail) are neither used nor written. */
+typedef struct {
+    const int *cu_seqlens;
+    int nseq, tokens;
+} ssd_packed;
+
+/* Carried states in pools of slots.  Sequence i starts from slot slots_in[i] of
+ * pool_in (a negative index, or pool_in NULL: from zero) and leaves the state
+ * after its last token in slot slots_out[i] of pool_out (negative, or pool_out
+ * NULL: not stored).  slots_in / slots_out are DEVICE arrays of nseq ints; NULL
+ * means slot i.  pool_in and pool_out may be the same buffer, and a sequence
+ * may end in the slot it started from; no other sequence of the call may start
+ * from a slot that one of them writes.  An empty sequence passes its state
+ * on.  A slot index past n_in / n_out counts as no slot, and a slot that two
+ * sequences would write is written by neither; both are recorded in the
+ * status word, as are offsets that are not ascending
+ * (ssd_workspace_status then returns SSD_ERR_INVALID_ARG). */
+typedef struct {
+    const void *pool_in;
+    void *pool_out;
+    const int *slots_in, *slots_out;
+    int n_in, n_out;          /* slots of each pool */
+} ssd_slots;
+
+/* The layer's depthwise causal convolution: in scan order (direction +1: as the
+ * rows lie; -1: each sequence from its last row back)
+ *
+ *     y_k = act(bias + sum_j w[:, width-1-j] * x_{k-j}),  j = 0 .. width-1
+ *
+ * with act = SiLU (silu != 0) or the identity, and x_k of k < 0 from the state,
+ * zero without one.  x, y: rows of `channels` io elements, ldx / ldy elements
+ * apart (>= channels); w [channels][width] and bias [channels] (or NULL)
+ * float32; arithmetic in float32, y rounded once.  The state of a slot is
+ * [width-1][channels] io elements, the last inputs in scan order, oldest first.
+ * x may not overlap y.  width 1..8.  The workspace may be NULL; otherwise it is
+ * the 256-byte status area.  16-byte (float32) or 8-byte (bf16) aligned rows
+ * with channels % 4 == 0 take the vector form. */
+typedef struct {
+    int channels, width, direction, silu;
+    ssd_dtype io;
+} ssd_conv_shape;
+
+ssd_status ssd_conv(const ssd_conv_shape *shape, const ssd_packed *seq, const void *x, long long ldx, const float *w,
+                    const float *bias, const ssd_slots *state, void *y, long long ldy, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/* Gradients of ssd_conv with zero starting states, for dL/dy = gy (io):
+ *     gx  dL/dx, io elements, rows ldgx apart (zero in rows of no sequence)
+ *     gw  [channels][width], gb [channels] (or NULL), float32: summed over all tokens
+ * The sums have a fixed order: equal inputs give equal bits.  Workspace of
+ * ssd_conv_bwd_workspace_bytes, 256-byte aligned, its status word zero on entry. */
+size_t ssd_conv_bwd_workspace_bytes(const ssd_conv_shape *shape, int tokens);
+ssd_status ssd_conv_bwd(const ssd_conv_shape *shape, const ssd_packed *seq, const void *x, long long ldx, const float *w,
+                        const float *bias, const void *gy, long long ldg, void *gx, long long ldgx, float *gw, float *gb,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/* The scan (ssd_scan's recurrence) over packed ragged sequences, any lengths.
+ * x, y rows of nheads*headdim, dt of nheads, B and C of ngroups*dstate io
+ * elements, each with its own row stride in elements, so x, B and C may be
+ * column blocks of one packed convolution output.  dt_bias NULL: dt is positive
+ * already; otherwise softplus(dt + dt_bias) is used.  A [nheads] is <= 0, D and
+ * dt_bias [nheads] may be NULL; all float32.  States: float32
+ * [nheads][headdim][dstate] a slot.  headdim in {16,32,64}, dstate in
+ * {16,32,64,128}.  y may not overlap an input.  Workspace of
+ * ssd_ragged_workspace_bytes, 256-byte aligned, status word zero on entry. */
+typedef struct {
+    int nheads, headdim, dstate, ngroups;
+    ssd_dtype io;
+} ssd_ragged_shape;
+typedef struct {
+    const void *x, *dt, *B, *C;
+    long long ldx, lddt, ldB, ldC;
+    const float *A, *D, *dt_bias;
+} ssd_ragged_params;
+
+size_t ssd_ragged_workspace_bytes(const ssd_ragged_shape *shape, int tokens, int nseq);
+ssd_status ssd_scan_ragged(const ssd_ragged_shape *shape, const ssd_packed *seq, const ssd_ragged_params *p, int direction,
+                           const ssd_slots *state, void *y, long long ldy, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/* One token of the layer for each of `rows` sequences, forward direction, both
+ * states updated in place in the layouts above:
+ *
+ *     x | B | C = silu(conv_b + conv_w . [conv_state | xBC]),  dt' = softplus(dt + dt_bias)
+ *     S <- exp(dt' A) S + dt' x (outer) B,    y = C S + D x
+ *
+ * xBC rows of nheads*headdim + 2*ngroups*dstate, dt of nheads, y of
+ * nheads*headdim io elements.  conv_state [n_slots][d_conv-1][channels] io,
+ * ssm_state [n_slots][nheads][headdim][dstate] float32, 16-byte aligned.  slots:
+ * a DEVICE array of `rows` ints, or NULL for slot r.  A row with a negative slot
+ * is padding: its y and all states are left as they were; so is a row whose slot
+ * is past n_slots or named by a second row (recorded in the status word).
+ * Between the convolution and the recurrence nothing is rounded: ssd_conv with a
+ * bf16 output rounds x, B and C there.  conv_b, dt_bias and D may be NULL. */
+typedef struct {
+    int rows, n_slots;
+    int nheads, headdim, dstate, ngroups, d_conv;
+    ssd_dtype io;
+} ssd_step_shape;
+
+size_t ssd_step_workspace_bytes(const ssd_step_shape *shape);
+ssd_status mamba2_step(const ssd_step_shape *shape, const void *xBC, long long ldx, const void *dt, long long lddt,
+                       const float *conv_w, const float *conv_b, const float *dt_bias, const float *A, const float *D,
+                       void *conv_state, float *ssm_state, const int *slots, void *y, long long ldy, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
