@@ -21,6 +21,7 @@ On packed ragged batches and single tokens (``layers.py``):
   ssd_conv_bwd(x, w, bias, gy, cu_seqlens)                    its gradients
   ssd_scan_ragged(x, dt, A, B, C, D, cu_seqlens)              the scan over packed sequences of any lengths
   mamba2_step(xBC, dt, ..., conv_state, ssm_state, slots)     one token of the layer per row
+  ffn_block(u, W_in, W_out) / ffn_block_bwd(..., gu, gy)      the gated feed-forward block, and its gradients
 """
 from __future__ import annotations
 
@@ -32,7 +33,8 @@ import torch
 __all__ = ["ssd_scan", "ssd_scan_state", "ssd_scan_bwd", "bidir_ssd", "r2l_block_scan", "bidir_ssd_noalloc", "noalloc_status", "NoallocArea", "workspace_bytes", "path_for",
            "segments_for", "kernel_launches", "mixer_bidir", "mixer_workspace_bytes", "gemm_bf16", "attention",
            "attention_block", "attention_block_workspace_bytes", "ssd_conv", "ssd_conv_bwd", "ssd_scan_ragged",
-           "ragged_workspace_bytes", "mamba2_step", "step_workspace_bytes", "workspace_status", "SSDError", "library_path", "lib"]
+           "ragged_workspace_bytes", "mamba2_step", "step_workspace_bytes", "ffn_block", "ffn_block_bwd",
+           "ffn_workspace_bytes", "ffn_bwd_workspace_bytes", "workspace_status", "SSDError", "library_path", "lib"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libbidirssd.so")
@@ -467,5 +469,6 @@ def noalloc_status(area: NoallocArea) -> None:
             _check(lib.ssd_workspace_status(int(area), 256, _stream(torch.device("cuda", area.device))))
 
 
-from .layers import (mamba2_step, ragged_workspace_bytes, ssd_conv, ssd_conv_bwd, ssd_scan_ragged,  # noqa: E402
+from .layers import (ffn_block, ffn_block_bwd, ffn_bwd_workspace_bytes, ffn_workspace_bytes, mamba2_step,  # noqa: E402
+                     ragged_workspace_bytes, ssd_conv, ssd_conv_bwd, ssd_scan_ragged,  # noqa: E402
                      step_workspace_bytes)

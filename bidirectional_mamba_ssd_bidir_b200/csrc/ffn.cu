@@ -1,0 +1,551 @@
+// ffn.cu -- the gated feed-forward block and its gradients on the tensor core.
+//
+// With g = u Wg^T and p = u Wu^T (Wg, Wu the two halves of W_in), h = act(g) * p, out = h Wd^T
+// (Wd = W_out):
+//
+//   gh = gy Wd        gg = gh p act'(g)      gp = gh act(g)
+//   gu = [gg gp] W_in          gW_in = [gg gp]^T u          gW_out = gy^T h
+//
+// act = SiLU: g sg, act' = sg (1 + g (1 - sg)); or GELU: g Phi(g), act' = Phi(g) + g phi(g).
+//
+// Three launches forward and backward together do all of it: the two projections, the activation and
+// the product in one kernel (h, and the projections when they are saved); gh with the activation's
+// gradient in its epilogue; and the three remaining products of the backward pass side by side.
+// Rounded to bf16 between them: h, gg, gp and the saved projections (the operands of the next
+// product have to be bf16 for the tensor core; accumulation, activation and its derivative are
+// float32).
+//
+// k_ffn, one kernel for all products D[M][N] = A B: persistent, warp-specialised, tiles of
+// 128 CG x 256 over a group of CG CTAs (CG = 2: a CTA pair shares one tcgen05.mma of M = 256, each
+// CTA holding half of A's rows and half of B's columns).  Warp 0 feeds the stage ring by TMA, warp 1
+// of the group's first CTA issues the MMAs (N 256, K 16), warps 2-5 drain one 256-column TMEM
+// accumulator while the other fills, each warp storing its own 32 rows through its own staging boxes.
+// An operand may lie along K (K-major: rows of 64 k, the descriptor's usual form) or across it
+// (MN-major: 64 x 64 boxes, 64 rows or columns wide), so nothing is transposed in memory.  Edges of
+// any size come out of the tensor maps: loads outside a matrix read zero, stores there are dropped.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cstring>
+
+#include "ffn.cuh"
+#include "ragged.cuh"
+#include "ssd_tc_common.cuh"
+
+namespace ssd {
+namespace {
+
+enum Epi { EPI_PLAIN, EPI_GLU, EPI_GLU_BWD };
+
+constexpr int kFK = 64;                          // K of a stage
+constexpr uint32_t kFBox = 128 * 128;            // 128 rows of 64 bf16
+constexpr uint32_t kFOutBox = 32 * 128;          // one warp's 32 rows of 64 columns
+constexpr int kFThreads = 192, kFMaxProb = 3;
+
+template <int EPI, int CG> struct FfnTile {
+    static constexpr uint32_t kA = kFBox, kB = CG == 2 ? kFBox : 2 * kFBox, kStage = kA + kB;
+    static constexpr int kBoxes = EPI == EPI_PLAIN ? 2 : 3;       // staging boxes of an epilogue warp
+    static constexpr int kStages = CG == 2 ? (EPI == EPI_PLAIN ? 6 : 5) : (EPI == EPI_PLAIN ? 4 : 3);
+    static constexpr uint32_t kOut = kStages * kStage;
+    static constexpr uint32_t kBar = kOut + 4 * kBoxes * kFOutBox;
+    static constexpr int kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + 2, kDone = kAccEmpty + 2,
+                         kBars = kDone + 1;
+    static constexpr uint32_t kMisc = (kBar + kBars * 8 + 15) & ~15u;
+    static constexpr uint32_t kSmem = kMisc + 32 + 1024;
+    static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+// One product of a launch.  a, b: the operands' maps; b2: the second half of B's columns where it is
+// another block of rows (the up projection); d: the outputs' maps (D; or h, gate, up; or gg, gp, h).
+struct FfnProb {
+    CUtensorMap a, b, d[3];
+    int M, N, K, a_mn, b_mn;
+    int up_row;                    // EPI_GLU: first row of the up projection in W_in
+    int tiles_m, tiles_n, tile0;   // its tiles, and the first one's number in the launch
+};
+struct FfnParams {
+    FfnProb p[kFMaxProb];
+    int nprob, ntiles, save, gelu;
+    const __nv_bfloat16 *gu;       // EPI_GLU_BWD: [M][2N]
+    int *status;
+    long long wait_cycles;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_in_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The forms for a pair: M = 256 across two CTAs, barriers in the first one.
+template <int CG> __device__ __forceinline__ void pair_load(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar) {
+    if constexpr (CG == 1) tma_load_2d(dst, map, c0, c1, bar);
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+            : "memory");
+}
+template <int CG> __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    if constexpr (CG == 1) mma_ss_w(d, a, b, id, acc);
+    else
+        asm volatile(
+            "{\n\t.reg .pred P, p;\n\telect.sync _|P, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "@P tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(id), "r"(acc));
+}
+// arrives on the barrier at this offset of every CTA of the group once the MMAs issued so far are done
+template <int CG> __device__ __forceinline__ void pair_commit(uint32_t bar) {
+    if constexpr (CG == 1) mma_commit_w(bar);
+    else
+        asm volatile(
+            "{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\t"
+            "@P tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+            "h"((uint16_t)3)
+            : "memory");
+}
+
+// The tile of number t: problem, first row and column.  Blocks of 8 row tiles walk along the columns,
+// so the tiles in flight at one time share their rows of A and columns of B in L2.
+struct FfnWhere {
+    int p, m0, n0;
+};
+template <int CG> __device__ __forceinline__ FfnWhere tile_at(const FfnParams &prm, int t, int width) {
+    int p = 0;
+    while (p + 1 < prm.nprob && t >= prm.p[p + 1].tile0) ++p;
+    const FfnProb &q = prm.p[p];
+    const int i = t - q.tile0, band = 8 * q.tiles_n, b = i / band, r = i % band;
+    const int rows = min(8, q.tiles_m - 8 * b);
+    return {p, (8 * b + r % rows) * 128 * CG, (r / rows) * width};
+}
+
+// act(g), act'(g)
+__device__ __forceinline__ void activation(const float (&g)[4], int gelu, float (&act)[4], float (&der)[4]) {
+    if (gelu) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float cdf = 0.5f * (1.f + erff(g[i] * 0.7071067811865476f));
+            act[i] = g[i] * cdf;
+            der[i] = fmaf(g[i] * 0.3989422804014327f, ex2a(-0.7213475204444817f * g[i] * g[i]), cdf);
+        }
+    } else {
+        float sg[4];
+        sigmoids<4>(g, sg);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            act[i] = g[i] * sg[i];
+            der[i] = sg[i] * fmaf(g[i], 1.f - sg[i], 1.f);
+        }
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float *v) {
+    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+
+template <int EPI, int CG>
+__global__ void __launch_bounds__(kFThreads, 1) k_ffn(const __grid_constant__ FfnParams prm) {
+    using L = FfnTile<EPI, CG>;
+    constexpr int S = L::kStages;
+    constexpr int kTileN = EPI == EPI_GLU ? 128 : 256;   // output columns of a tile
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(sm);
+    auto bar = [&](int i) { return sbase + L::kBar + 8u * i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::kMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kMisc + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+    const int first = blockIdx.x / CG, step = gridDim.x / CG;
+    const uint32_t MASK = 0xffffffffu;
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        *reinterpret_cast<volatile long long *>(abort_flag + 1) = prm.wait_cycles;
+        for (int i = 0; i < L::kBars; ++i) mbar_init(bar(i), (i == L::kAccEmpty || i == L::kAccEmpty + 1) ? 4u * CG : 1u);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        if constexpr (CG == 2) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_slot)));
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (CG == 2) cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA loads (each CTA its own half)
+        if (lane == 0) {
+            long long g = 0;
+            bool ok = true;
+            for (int t = first; t < prm.ntiles && ok; t += step) {
+                const FfnWhere w = tile_at<CG>(prm, t, kTileN);
+                const FfnProb &q = prm.p[w.p];
+                const int m = w.m0 + 128 * rank, nk = (q.K + kFK - 1) / kFK;
+                for (int kt = 0; kt < nk; ++kt, ++g) {
+                    const int st = (int)(g % S);
+                    if (g >= S && !(ok = mbar_wait(bar(L::kEmpty + st), (uint32_t)((g / S) - 1) & 1, 1u, abort_flag,
+                                                   prm.status, 141)))
+                        break;
+                    // the stage is complete when both CTAs' bytes have landed
+                    const uint32_t full = CG == 2 ? in_cta(bar(L::kFull + st), 0) : bar(L::kFull + st);
+                    if (rank == 0) mbar_expect_tx(bar(L::kFull + st), CG * L::kStage);
+                    const uint32_t sa = sbase + st * L::kStage, sb = sa + L::kA;
+                    const int k0 = kt * kFK;
+                    if (q.a_mn) {
+                        pair_load<CG>(sa, &q.a, m, k0, full);
+                        pair_load<CG>(sa + kFBox / 2, &q.a, m + 64, k0, full);
+                    } else {
+                        pair_load<CG>(sa, &q.a, k0, m, full);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2 / CG; ++h) {
+                        const int half = CG == 2 ? (int)rank : h;   // which 128 columns of the tile's 256
+                        const uint32_t dst = sb + h * kFBox;
+                        if (EPI == EPI_GLU) {
+                            pair_load<CG>(dst, &q.b, k0, w.n0 + half * q.up_row, full);
+                        } else if (q.b_mn) {
+                            pair_load<CG>(dst, &q.b, w.n0 + 128 * half, k0, full);
+                            pair_load<CG>(dst + kFBox / 2, &q.b, w.n0 + 128 * half + 64, k0, full);
+                        } else {
+                            pair_load<CG>(dst, &q.b, k0, w.n0 + 128 * half, full);
+                        }
+                    }
+                }
+            }
+            if (*abort_flag && rank == 0)
+                for (long long x = g - 1; x >= 0 && x >= g - S; --x)
+                    mbar_drain(bar(L::kFull + (int)(x % S)), (uint32_t)(x / S) & 1, prm.wait_cycles);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMAs
+        if (rank == 0) {
+            long long g = 0;
+            int tc = 0;
+            bool ok = true;
+            for (int t = first; t < prm.ntiles && ok; t += step, ++tc) {
+                const FfnProb &q = prm.p[tile_at<CG>(prm, t, kTileN).p];
+                const int nk = (q.K + kFK - 1) / kFK, acc = tc & 1;
+                // M 128 CG, N 256
+                const uint32_t id = (idesc(256, q.a_mn, q.b_mn) & ~(31u << 24)) | ((uint32_t)(128 * CG >> 4) << 24);
+                // K-major: rows of 128 bytes, 16 k = 32 bytes on; MN-major: boxes of 64 x 64 (8 KB
+                // apart), 16 k = 16 rows of 128 bytes on
+                const uint32_t la = q.a_mn ? kFBox / 2 : 16, lb = q.b_mn ? kFBox / 2 : 16;
+                const uint32_t ka = q.a_mn ? 2048 : 32, kb = q.b_mn ? 2048 : 32;
+                if (tc >= 2 && !(ok = mbar_wait(bar(L::kAccEmpty + acc), ((tc >> 1) - 1) & 1, MASK, abort_flag, prm.status, 142)))
+                    break;
+                tc_fence_after();
+                for (int kt = 0; kt < nk; ++kt, ++g) {
+                    const int st = (int)(g % S);
+                    if (!(ok = mbar_wait(bar(L::kFull + st), (uint32_t)(g / S) & 1, MASK, abort_flag, prm.status, 143))) break;
+                    tc_fence_after();
+                    const uint32_t sa = sbase + st * L::kStage;
+                    const SDesc da = make_sdesc(sa, la, 1024), db = make_sdesc(sa + L::kA, lb, 1024);
+#pragma unroll
+                    for (int ks = 0; ks < kFK / 16; ++ks)
+                        pair_mma<CG>(tmem + 256u * acc, da.at(ks * ka), db.at(ks * kb), id, (kt | ks) != 0);
+                    pair_commit<CG>(bar(L::kEmpty + st));
+                }
+                if (!ok) break;
+                pair_commit<CG>(bar(L::kAccFull + acc));
+            }
+            pair_commit<CG>(bar(L::kDone));
+        }
+        // both CTAs leave only after every MMA issued has completed
+        if (lane == 0) mbar_drain(bar(L::kDone), 0, prm.wait_cycles);
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int qd = warp & 3;
+        const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16);
+        const uint32_t boxes = L::kOut + (uint32_t)(warp - 2) * L::kBoxes * kFOutBox;
+        int tc = 0, used = 0;                     // tiles; boxes handed to a store so far
+        // box number `used` of the warp's ring, free again
+        auto box = [&]() { return boxes + (uint32_t)(used % L::kBoxes) * kFOutBox; };
+        auto put = [&](uint32_t b, int c8, const float *v) {   // 8 columns (chunk c8) of this thread's row
+            *reinterpret_cast<uint4 *>(sm + b + swz(lane, c8)) = pack8(v);
+        };
+        auto send = [&](const CUtensorMap *map, uint32_t b, int n, int m) {
+            if (lane == 0) tma_store_2d(map, sbase + b, n, m);
+        };
+        for (int t = first; t < prm.ntiles; t += step, ++tc) {
+            const FfnWhere w = tile_at<CG>(prm, t, kTileN);
+            const FfnProb &q = prm.p[w.p];
+            const int acc = tc & 1, m0 = w.m0 + 128 * rank + 32 * qd;
+            if (!mbar_wait(bar(L::kAccFull + acc), (tc >> 1) & 1, MASK, abort_flag, prm.status, 144)) break;
+            tc_fence_after();
+            const uint32_t ta = tl + 256u * acc;
+#pragma unroll 1
+            for (int c = 0; c < kTileN; c += 64) {
+                // boxes of this round are free once all but the rounds' stores in flight have been read
+                const bool live = w.n0 + c < q.N;
+                if (EPI == EPI_PLAIN) {
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    __syncwarp();
+                    const uint32_t b = box();
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float v[32];
+                        tmem_ld32(ta + c + 32 * x, v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) put(b, 4 * x + i, v + 8 * i);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (live) send(&q.d[0], b, w.n0 + c, m0);
+                    if (lane == 0) bulk_commit();
+                    ++used;
+                } else if (EPI == EPI_GLU) {
+                    if (lane == 0) bulk_wait_read0();
+                    __syncwarp();
+                    const uint32_t b = boxes;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float vg[32], vu[32];
+                        tmem_ld32x2(ta + c + 32 * x, ta + 128 + c + 32 * x, vg, vu);
+                        if (prm.save) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                put(b + kFOutBox, 4 * x + i, vg + 8 * i);
+                                put(b + 2 * kFOutBox, 4 * x + i, vu + 8 * i);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float g4[4] = {vg[4 * i], vg[4 * i + 1], vg[4 * i + 2], vg[4 * i + 3]};
+                            float act[4], der[4];
+                            activation(g4, prm.gelu, act, der);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) vu[4 * i + e] *= act[e];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) put(b, 4 * x + i, vu + 8 * i);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (live) {
+                        send(&q.d[0], b, w.n0 + c, m0);
+                        if (prm.save) {
+                            send(&q.d[1], b + kFOutBox, w.n0 + c, m0);
+                            send(&q.d[2], b + 2 * kFOutBox, w.n0 + c, m0);
+                        }
+                    }
+                    if (lane == 0) bulk_commit();
+                } else {
+                    const uint32_t b = boxes;
+                    const int m = m0 + lane;
+                    const __nv_bfloat16 *row = prm.gu + (long long)m * 2 * q.N + w.n0 + c;
+                    uint4 rg[8], ru[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        rg[i] = ru[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (m < q.M && w.n0 + c + 8 * i < q.N) {   // N is a multiple of 8
+                            rg[i] = *reinterpret_cast<const uint4 *>(row + 8 * i);
+                            ru[i] = *reinterpret_cast<const uint4 *>(row + q.N + 8 * i);
+                        }
+                    }
+                    if (lane == 0) bulk_wait_read0();
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float gh[32];
+                        tmem_ld32(ta + c + 32 * x, gh);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 a = rg[4 * x + i], u = ru[4 * x + i];
+                            const uint32_t ga[4] = {a.x, a.y, a.z, a.w}, ua[4] = {u.x, u.y, u.z, u.w};
+                            float gg[8], gp[8], hh[8];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float g4[4] = {bf16lo(ga[2 * e]), bf16hi(ga[2 * e]), bf16lo(ga[2 * e + 1]), bf16hi(ga[2 * e + 1])};
+                                const float u4[4] = {bf16lo(ua[2 * e]), bf16hi(ua[2 * e]), bf16lo(ua[2 * e + 1]), bf16hi(ua[2 * e + 1])};
+                                float act[4], der[4];
+                                activation(g4, prm.gelu, act, der);
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) {
+                                    const float d = gh[8 * i + 4 * e + z];
+                                    gg[4 * e + z] = d * u4[z] * der[z];
+                                    gp[4 * e + z] = d * act[z];
+                                    hh[4 * e + z] = act[z] * u4[z];
+                                }
+                            }
+                            put(b, 4 * x + i, gg);
+                            put(b + kFOutBox, 4 * x + i, gp);
+                            put(b + 2 * kFOutBox, 4 * x + i, hh);
+                        }
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (live) {
+                        send(&q.d[0], b, w.n0 + c, m0);
+                        send(&q.d[1], b + kFOutBox, w.n0 + c, m0);
+                        send(&q.d[2], b + 2 * kFOutBox, w.n0 + c, m0);
+                    }
+                    if (lane == 0) bulk_commit();
+                }
+            }
+            // the accumulator has been read: the MMA warp may fill it again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2) arrive_in_cluster(in_cta(bar(L::kAccEmpty + acc), 0));
+                else mbar_arrive(bar(L::kAccEmpty + acc));
+            }
+        }
+        if (lane == 0) bulk_wait0();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    // the pair ends together: a CTA's barriers are signalled by the other one until then
+    if constexpr (CG == 2) cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after();
+        if constexpr (CG == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+// [rows][cols] bf16, rows `ld` elements apart; box [box_rows][64], 128-byte swizzle
+bool map_of(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+    EncodeTiled enc = get_encode();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * 2};
+    const cuuint32_t box[2] = {64, box_rows}, estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Operand maps: X [M or N][K] K-major, or its transpose [K][M or N] (mn)
+bool operand(CUtensorMap *m, const void *x, int n, int k, bool mn) {
+    return mn ? map_of(m, x, k, n, n, 64) : map_of(m, x, n, k, k, 128);
+}
+
+template <int EPI, int CG> cudaError_t run_ffn(FfnParams &prm, cudaStream_t st) {
+    const int width = EPI == EPI_GLU ? 128 : 256;
+    prm.ntiles = 0;
+    for (int i = 0; i < prm.nprob; ++i) {
+        FfnProb &q = prm.p[i];
+        q.tiles_m = (q.M + 128 * CG - 1) / (128 * CG);
+        q.tiles_n = (q.N + width - 1) / width;
+        q.tile0 = prm.ntiles;
+        const long long n = (long long)q.tiles_m * q.tiles_n + prm.ntiles;
+        if (n > 0x7fffffff) return cudaErrorInvalidValue;
+        prm.ntiles = (int)n;
+    }
+    auto *kernel = k_ffn<EPI, CG>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FfnTile<EPI, CG>::kSmem);
+    if (e != cudaSuccess) return e;
+    int dev = 0, sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const int groups = prm.ntiles < sms / CG ? prm.ntiles : sms / CG;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = CG;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(groups * CG);
+    cfg.blockDim = dim3(kFThreads);
+    cfg.dynamicSmemBytes = FfnTile<EPI, CG>::kSmem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, prm);
+}
+
+// CTA pairs once there are two row tiles to pair.
+template <int EPI> cudaError_t run_ffn_any(FfnParams &prm, cudaStream_t st) {
+    int m = 0;
+    for (int i = 0; i < prm.nprob; ++i) m = prm.p[i].M > m ? prm.p[i].M : m;
+    return m > 128 ? run_ffn<EPI, 2>(prm, st) : run_ffn<EPI, 1>(prm, st);
+}
+
+FfnProb product(int M, int N, int K, bool a_mn, bool b_mn) {
+    FfnProb q;
+    memset(&q, 0, sizeof q);
+    q.M = M; q.N = N; q.K = K; q.a_mn = a_mn; q.b_mn = b_mn;
+    return q;
+}
+
+}  // namespace
+
+bool ffn_supported() { return get_encode() != nullptr; }
+
+cudaError_t launch_ffn(const FfnArgs &a, cudaStream_t st) {
+    FfnParams prm;
+    memset(&prm, 0, sizeof prm);
+    prm.nprob = 1; prm.gelu = a.gelu; prm.status = a.status; prm.wait_cycles = a.wait_cycles;
+    prm.save = a.gu != nullptr;
+    FfnProb &q = prm.p[0];
+    q = product(a.T, a.F, a.D, false, false);
+    q.up_row = a.F;
+    bool ok = operand(&q.a, a.u, a.T, a.D, false) && operand(&q.b, a.W_in, 2 * a.F, a.D, false) &&
+              map_of(&q.d[0], a.h, a.T, a.F, a.F, 32);
+    if (a.gu)
+        ok = ok && map_of(&q.d[1], a.gu, a.T, a.F, 2ull * a.F, 32) &&
+             map_of(&q.d[2], static_cast<__nv_bfloat16 *>(a.gu) + a.F, a.T, a.F, 2ull * a.F, 32);
+    if (!ok) return cudaErrorInvalidValue;
+    cudaError_t e = run_ffn_any<EPI_GLU>(prm, st);
+    if (e != cudaSuccess) return e;
+    q = product(a.T, a.D, a.F, false, false);
+    if (!operand(&q.a, a.h, a.T, a.F, false) || !operand(&q.b, a.W_out, a.D, a.F, false) || !map_of(&q.d[0], a.out, a.T, a.D, a.D, 32))
+        return cudaErrorInvalidValue;
+    return run_ffn_any<EPI_PLAIN>(prm, st);
+}
+
+cudaError_t launch_ffn_bwd(const FfnArgs &a, cudaStream_t st) {
+    FfnParams prm;
+    memset(&prm, 0, sizeof prm);
+    prm.nprob = 1; prm.gelu = a.gelu; prm.status = a.status; prm.wait_cycles = a.wait_cycles;
+    prm.gu = static_cast<const __nv_bfloat16 *>(a.gu);
+    FfnProb &q = prm.p[0];
+    // gh = gy Wd, then the activation's gradient
+    q = product(a.T, a.F, a.D, false, true);
+    __nv_bfloat16 *ggu = static_cast<__nv_bfloat16 *>(a.ggu);
+    if (!operand(&q.a, a.gy, a.T, a.D, false) || !operand(&q.b, a.W_out, a.F, a.D, true) ||
+        !map_of(&q.d[0], ggu, a.T, a.F, 2ull * a.F, 32) || !map_of(&q.d[1], ggu + a.F, a.T, a.F, 2ull * a.F, 32) ||
+        !map_of(&q.d[2], a.h, a.T, a.F, a.F, 32))
+        return cudaErrorInvalidValue;
+    cudaError_t e = run_ffn_any<EPI_GLU_BWD>(prm, st);
+    if (e != cudaSuccess) return e;
+    // the longest products first: their tiles end last otherwise
+    prm.nprob = 3;
+    prm.p[0] = product(a.T, a.D, 2 * a.F, false, true);
+    prm.p[1] = product(2 * a.F, a.D, a.T, true, true);
+    prm.p[2] = product(a.D, a.F, a.T, true, true);
+    if (!operand(&prm.p[0].a, ggu, a.T, 2 * a.F, false) || !operand(&prm.p[0].b, a.W_in, a.D, 2 * a.F, true) ||
+        !map_of(&prm.p[0].d[0], a.gu_, a.T, a.D, a.D, 32) ||
+        !operand(&prm.p[1].a, ggu, 2 * a.F, a.T, true) || !operand(&prm.p[1].b, a.u, a.D, a.T, true) ||
+        !map_of(&prm.p[1].d[0], a.gW_in, 2 * a.F, a.D, a.D, 32) ||
+        !operand(&prm.p[2].a, a.gy, a.D, a.T, true) || !operand(&prm.p[2].b, a.h, a.F, a.T, true) ||
+        !map_of(&prm.p[2].d[0], a.gW_out, a.D, a.F, a.F, 32))
+        return cudaErrorInvalidValue;
+    return run_ffn_any<EPI_PLAIN>(prm, st);
+}
+
+}  // namespace ssd

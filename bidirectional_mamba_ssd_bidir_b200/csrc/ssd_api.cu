@@ -8,6 +8,7 @@
 
 #include "../../include/bidir_ssd.h"
 #include "attention.cuh"
+#include "ffn.cuh"
 #include "mixer.cuh"
 #include "ragged.cuh"
 #include "ssd_internal.cuh"
@@ -938,6 +939,93 @@ ssd_status ssd_scan_ragged(const ssd_ragged_shape *shape, const ssd_packed *seq,
     a.wait_cycles = wait_cycles_now();
     cudaError_t e = ssd::launch_ragged_simt(a, shape->io == SSD_BF16, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SSD_OK : cuda_fail(e, "ragged scan launch");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- the gated feed-forward block
+
+namespace {
+
+ssd_status ffn_checks(const ssd_ffn_shape *s) {
+    if (!s) return fail(SSD_ERR_INVALID_ARG, "shape is NULL");
+    if (s->tokens < 0 || s->d_model <= 0 || s->d_ff <= 0) return fail(SSD_ERR_INVALID_ARG, "negative or zero size in shape");
+    if (s->activation != SSD_ACT_SILU && s->activation != SSD_ACT_GELU)
+        return fail(SSD_ERR_INVALID_ARG, "unknown activation %d", (int)s->activation);
+    if (s->d_model % 8 != 0 || s->d_ff % 8 != 0)
+        return fail(SSD_ERR_UNSUPPORTED, "feed-forward block needs d_model and d_ff multiples of 8");
+    if (s->d_ff > (1 << 28) || s->d_model > (1 << 28)) return fail(SSD_ERR_UNSUPPORTED, "d_model and d_ff up to 2^28");
+    return SSD_OK;
+}
+
+size_t ffn_h_bytes(const ssd_ffn_shape *s) { return round_up((size_t)s->tokens * s->d_ff * 2); }
+
+ssd_status check_ws(const void *ws, size_t bytes, size_t need) {
+    if (!ws || !aligned(ws, kAlign)) return fail(SSD_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
+    if (bytes < need) return fail(SSD_ERR_INVALID_ARG, "workspace %zu bytes < %zu needed", bytes, need);
+    return SSD_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssd_ffn_workspace_bytes(const ssd_ffn_shape *shape) {
+    return ffn_checks(shape) == SSD_OK ? kStatusBytes + ffn_h_bytes(shape) : 0;
+}
+size_t ssd_ffn_bwd_workspace_bytes(const ssd_ffn_shape *shape) {
+    return ffn_checks(shape) == SSD_OK ? kStatusBytes + 3 * ffn_h_bytes(shape) : 0;
+}
+
+ssd_status ffn_block(const ssd_ffn_shape *shape, const void *u, const void *W_in, const void *W_out, void *out, void *gu,
+                     void *workspace, size_t workspace_bytes, void *stream) {
+    g_err.clear();
+    ssd_status st = ffn_checks(shape);
+    if (st != SSD_OK) return st;
+    if (shape->tokens == 0) return SSD_OK;
+    if (!aligned16(u) || !aligned16(W_in) || !aligned16(W_out) || !aligned16(out) || !aligned(gu, 16))
+        return fail(SSD_ERR_INVALID_ARG, "u, W_in, W_out, out (and gu) must be 16-byte aligned");
+    if ((st = check_ws(workspace, workspace_bytes, ssd_ffn_workspace_bytes(shape))) != SSD_OK) return st;
+    if (!ssd::ffn_supported()) return fail(SSD_ERR_UNSUPPORTED, "the TMA encoder is unavailable");
+    ssd::FfnArgs a{};
+    a.T = shape->tokens; a.D = shape->d_model; a.F = shape->d_ff; a.gelu = shape->activation == SSD_ACT_GELU;
+    a.u = u; a.W_in = W_in; a.W_out = W_out; a.out = out; a.gu = gu;
+    a.h = static_cast<char *>(workspace) + kStatusBytes;
+    a.status = static_cast<int *>(workspace);
+    a.wait_cycles = wait_cycles_now();
+    cudaError_t e = ssd::launch_ffn(a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? SSD_OK : cuda_fail(e, "feed-forward launch");
+}
+
+ssd_status ffn_block_bwd(const ssd_ffn_shape *shape, const void *u, const void *W_in, const void *W_out, const void *gu,
+                         const void *gy, void *g_u, void *gW_in, void *gW_out, void *workspace, size_t workspace_bytes,
+                         void *stream) {
+    g_err.clear();
+    ssd_status st = ffn_checks(shape);
+    if (st != SSD_OK) return st;
+    if (!aligned16(gW_in) || !aligned16(gW_out)) return fail(SSD_ERR_INVALID_ARG, "gW_in and gW_out must be 16-byte aligned");
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (shape->tokens == 0) {
+        const size_t n = (size_t)shape->d_model * shape->d_ff * 2;
+        cudaError_t e = cudaMemsetAsync(gW_in, 0, 2 * n, cs);
+        if (e == cudaSuccess) e = cudaMemsetAsync(gW_out, 0, n, cs);
+        return e == cudaSuccess ? SSD_OK : cuda_fail(e, "empty gradient clear");
+    }
+    if (!aligned16(u) || !aligned16(W_in) || !aligned16(W_out) || !aligned16(gu) || !aligned16(gy) || !aligned16(g_u))
+        return fail(SSD_ERR_INVALID_ARG, "u, W_in, W_out, gu, gy and g_u must be 16-byte aligned");
+    if ((st = check_ws(workspace, workspace_bytes, ssd_ffn_bwd_workspace_bytes(shape))) != SSD_OK) return st;
+    if (!ssd::ffn_supported()) return fail(SSD_ERR_UNSUPPORTED, "the TMA encoder is unavailable");
+    ssd::FfnArgs a{};
+    a.T = shape->tokens; a.D = shape->d_model; a.F = shape->d_ff; a.gelu = shape->activation == SSD_ACT_GELU;
+    a.u = u; a.W_in = W_in; a.W_out = W_out; a.gu = const_cast<void *>(gu); a.gy = gy;
+    a.gu_ = g_u; a.gW_in = gW_in; a.gW_out = gW_out;
+    char *ws = static_cast<char *>(workspace) + kStatusBytes;
+    a.h = ws;
+    a.ggu = ws + ffn_h_bytes(shape);
+    a.status = static_cast<int *>(workspace);
+    a.wait_cycles = wait_cycles_now();
+    cudaError_t e = ssd::launch_ffn_bwd(a, cs);
+    return e == cudaSuccess ? SSD_OK : cuda_fail(e, "feed-forward gradient launch");
 }
 
 }  // extern "C"

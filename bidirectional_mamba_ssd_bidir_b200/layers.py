@@ -5,6 +5,7 @@ Binding of the second half of ``include/bidir_ssd.h``:
   ssd_conv / ssd_conv_bwd     the causal convolution with carried states, and its gradients
   ssd_scan_ragged             the scan over packed ragged sequences, states in slots
   mamba2_step                 one token per row: convolution, SiLU, softplus, recurrence
+  ffn_block / ffn_block_bwd   the gated feed-forward block, and its gradients
 
 Packed batches: the rows of every tensor are the tokens of all sequences, one sequence behind
 another, and ``cu_seqlens`` (int32, on the device, ``nseq + 1`` entries) holds where each starts.
@@ -24,7 +25,8 @@ import torch
 
 from . import SSDError, _check, _stream, lib  # noqa: F401
 
-__all__ = ["ssd_conv", "ssd_conv_bwd", "ssd_scan_ragged", "ragged_workspace_bytes", "mamba2_step", "step_workspace_bytes"]
+__all__ = ["ssd_conv", "ssd_conv_bwd", "ssd_scan_ragged", "ragged_workspace_bytes", "mamba2_step", "step_workspace_bytes",
+           "ffn_block", "ffn_block_bwd", "ffn_workspace_bytes", "ffn_bwd_workspace_bytes"]
 
 _VP, _SZ, _LL, _I = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_longlong, ctypes.c_int
 
@@ -54,6 +56,10 @@ class _StepShape(ctypes.Structure):
     _fields_ = [(n, _I) for n in ("rows", "n_slots", "nheads", "headdim", "dstate", "ngroups", "d_conv", "io")]
 
 
+class _FfnShape(ctypes.Structure):
+    _fields_ = [(n, _I) for n in ("tokens", "d_model", "d_ff", "activation")]
+
+
 _P = ctypes.POINTER
 lib.ssd_conv.argtypes = [_P(_ConvShape), _P(_Packed), _VP, _LL, _VP, _VP, _P(_Slots), _VP, _LL, _VP, _SZ, _VP]
 lib.ssd_conv_bwd_workspace_bytes.argtypes = [_P(_ConvShape), _I]
@@ -65,7 +71,11 @@ lib.ssd_scan_ragged.argtypes = [_P(_RaggedShape), _P(_Packed), _P(_RaggedParams)
 lib.ssd_step_workspace_bytes.argtypes = [_P(_StepShape)]
 lib.ssd_step_workspace_bytes.restype = _SZ
 lib.mamba2_step.argtypes = [_P(_StepShape), _VP, _LL, _VP, _LL] + [_VP] * 8 + [_VP, _LL, _VP, _SZ, _VP]
-for _f in (lib.ssd_conv, lib.ssd_conv_bwd, lib.ssd_scan_ragged, lib.mamba2_step):
+lib.ssd_ffn_workspace_bytes.argtypes = lib.ssd_ffn_bwd_workspace_bytes.argtypes = [_P(_FfnShape)]
+lib.ssd_ffn_workspace_bytes.restype = lib.ssd_ffn_bwd_workspace_bytes.restype = _SZ
+lib.ffn_block.argtypes = [_P(_FfnShape)] + [_VP] * 6 + [_SZ, _VP]
+lib.ffn_block_bwd.argtypes = [_P(_FfnShape)] + [_VP] * 9 + [_SZ, _VP]
+for _f in (lib.ssd_conv, lib.ssd_conv_bwd, lib.ssd_scan_ragged, lib.mamba2_step, lib.ffn_block, lib.ffn_block_bwd):
     _f.restype = _I
 
 _IO = {torch.bfloat16: 0, torch.float32: 1}
@@ -320,3 +330,65 @@ def mamba2_step(xBC, dt, conv_w, conv_b, dt_bias, A, D, conv_state, ssm_state, s
           _f32("dt_bias", dt_bias, (H,), dev), _f32("A", A, (H,), dev), _f32("D", D, (H,), dev), vp, sp,
           _i32("slots", slots, R, dev), yp, ldy, wp, wn)
     return y
+
+
+_ACT = {"silu": 0, "gelu": 1}
+
+
+def _ffn_shape(u, W_in, W_out, activation, dev):
+    if activation not in _ACT:
+        raise ValueError(f"unknown activation {activation!r} (silu or gelu)")
+    if W_in.dim() != 2 or W_out.dim() != 2 or u.dim() < 1:
+        raise ValueError("u must be [..., d_model], W_in [2 d_ff, d_model], W_out [d_model, d_ff]")
+    D, F = W_out.shape
+    return _FfnShape(u.numel() // D if D else 0, D, F, _ACT[activation])
+
+
+def _bf16(name, t, shape, dev):
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous bf16 of shape {tuple(shape)} on {dev}")
+    return t.data_ptr()
+
+
+def ffn_workspace_bytes(tokens: int, d_model: int, d_ff: int) -> int:
+    """Workspace size of ffn_block (0: refused)."""
+    return int(lib.ssd_ffn_workspace_bytes(_FfnShape(tokens, d_model, d_ff, 0)))
+
+
+def ffn_bwd_workspace_bytes(tokens: int, d_model: int, d_ff: int) -> int:
+    """Workspace size of ffn_block_bwd (0: refused)."""
+    return int(lib.ssd_ffn_bwd_workspace_bytes(_FfnShape(tokens, d_model, d_ff, 0)))
+
+
+def ffn_block(u, W_in, W_out, activation: str = "silu", save: bool = False, out=None, workspace=None):
+    """The gated feed-forward block: out = (act(u Wg^T) * (u Wu^T)) W_out^T, with W_in = [Wg; Wu].
+
+    u [..., d_model] bf16, W_in [2 d_ff, d_model], W_out [d_model, d_ff]; activation "silu" or "gelu".
+    ``save``: return (out, gu), gu [..., 2 d_ff] the two projections that ffn_block_bwd needs."""
+    dev = _cuda("u", u)
+    shape = _ffn_shape(u, W_in, W_out, activation, dev)
+    D, F, lead = shape.d_model, shape.d_ff, u.shape[:-1]
+    up, wi, wo = _bf16("u", u, lead + (D,), dev), _bf16("W_in", W_in, (2 * F, D), dev), _bf16("W_out", W_out, (D, F), dev)
+    y = torch.empty(u.shape, dtype=torch.bfloat16, device=dev) if out is None else out
+    yp = _bf16("out", y, lead + (D,), dev)
+    if out is not None:
+        for name, t in (("u", u), ("W_in", W_in), ("W_out", W_out)):
+            if yp < t.data_ptr() + 2 * t.numel() and t.data_ptr() < yp + 2 * y.numel():
+                raise ValueError(f"out overlaps {name}")
+    gu = torch.empty(lead + (2 * F,), dtype=torch.bfloat16, device=dev) if save else None
+    ws, wp, wn = _scratch(workspace, max(256, lib.ssd_ffn_workspace_bytes(shape)), dev)
+    _call(dev, lib.ffn_block, shape, up, wi, wo, yp, gu.data_ptr() if save else None, wp, wn)
+    return (y, gu) if save else y
+
+
+def ffn_block_bwd(u, W_in, W_out, gu, gy, activation: str = "silu", workspace=None) -> dict:
+    """Gradients of ffn_block for dL/dout = gy, from the saved projections: dict of u, W_in, W_out (bf16)."""
+    dev = _cuda("u", u)
+    shape = _ffn_shape(u, W_in, W_out, activation, dev)
+    D, F, lead = shape.d_model, shape.d_ff, u.shape[:-1]
+    ptrs = [_bf16("u", u, lead + (D,), dev), _bf16("W_in", W_in, (2 * F, D), dev), _bf16("W_out", W_out, (D, F), dev),
+            _bf16("gu", gu, lead + (2 * F,), dev), _bf16("gy", gy, lead + (D,), dev)]
+    g = {"u": torch.empty_like(u), "W_in": torch.empty_like(W_in), "W_out": torch.empty_like(W_out)}
+    ws, wp, wn = _scratch(workspace, max(256, lib.ssd_ffn_bwd_workspace_bytes(shape)), dev)
+    _call(dev, lib.ffn_block_bwd, shape, *ptrs, g["u"].data_ptr(), g["W_in"].data_ptr(), g["W_out"].data_ptr(), wp, wn)
+    return g

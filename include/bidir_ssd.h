@@ -452,6 +452,46 @@ ssd_status mamba2_step(const ssd_step_shape *shape, const void *xBC, long long l
                        void *conv_state, float *ssm_state, const int *slots, void *y, long long ldy, void *workspace,
                        size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The gated feed-forward block.
+ *
+ * "DiffuMamba: High-Throughput Diffusion LMs with Mamba Backbone", technical
+ * summary section 2, replaces the attention mixer of a Transformer diffusion
+ * LM and says nothing of its feed-forward part; it is read as the gated block
+ * of current Transformers (no bias):
+ *
+ *   g | p = u W_in^T,   h = act(g) * p,   out = h W_out^T
+ *
+ * All bf16, row-major, contiguous, 16-byte aligned: u, out [tokens][d_model],
+ * W_in [2 d_ff][d_model] (the gate's rows, then the other projection's), W_out
+ * [d_model][d_ff]; accumulation and activation in float32; h is rounded to
+ * bf16 between the two products.  d_model and d_ff multiples of 8, any number
+ * of tokens.  SSD_ACT_GELU is the exact form g Phi(g).
+ * ------------------------------------------------------------------------ */
+typedef enum { SSD_ACT_SILU = 0, SSD_ACT_GELU = 1 } ssd_activation;
+
+typedef struct {
+    int tokens, d_model, d_ff;
+    ssd_activation activation;
+} ssd_ffn_shape;
+
+/* gu [tokens][2 d_ff] (or NULL) receives g | p, rounded to bf16, for
+ * ffn_block_bwd.  Workspace 256-byte aligned, of ssd_ffn_workspace_bytes (0 if
+ * the shape is refused), status word zero on entry.  out may not overlap an
+ * input. */
+size_t ssd_ffn_workspace_bytes(const ssd_ffn_shape *shape);
+ssd_status ffn_block(const ssd_ffn_shape *shape, const void *u, const void *W_in, const void *W_out, void *out, void *gu,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients of ffn_block for dL/dout = gy [tokens][d_model], from the saved
+ * projections gu: g_u like u, gW_in like W_in, gW_out like W_out (bf16, float32
+ * sums; written, not added to).  The gradients of g and p and h itself are
+ * rounded to bf16 between the products. */
+size_t ssd_ffn_bwd_workspace_bytes(const ssd_ffn_shape *shape);
+ssd_status ffn_block_bwd(const ssd_ffn_shape *shape, const void *u, const void *W_in, const void *W_out, const void *gu,
+                         const void *gy, void *g_u, void *gW_in, void *gW_out, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
 #ifdef __cplusplus
 }
 #endif
