@@ -87,6 +87,9 @@ inline int ragged_segment(long long tokens, long long ctas_per_segment, int quan
     return (int)(s < quant ? quant : s);
 }
 cudaError_t launch_ragged_simt(const RaggedArgs &a, bool bf16, cudaStream_t st);
+// The tensor-core form (ragged_tc.cu); its segments are whole chunks of 128 tokens.
+bool ragged_tc_supported(const RaggedArgs &a, bool bf16);
+cudaError_t launch_ragged_tc(const RaggedArgs &a, cudaStream_t st);
 
 #ifdef __CUDACC__
 namespace {

@@ -845,8 +845,9 @@ ssd_status ragged_plan(const ssd_ragged_shape *s, long long tokens, int nseq, Ra
     ssd_status st = check_heads(s->nheads, s->headdim, s->dstate, s->ngroups, s->io);
     if (st != SSD_OK) return st;
     if (tokens < 0 || nseq < 0 || tokens + nseq > 0x7fff0000LL) return fail(SSD_ERR_INVALID_ARG, "bad token or sequence count");
-    // segments for about four CTAs per SM
-    p->seg = ssd::ragged_segment(tokens, s->nheads, 64, 4 * 148);
+    // Tensor-core shapes: one CTA (two heads) to an SM, chunks of 128 tokens; others: about four CTAs to an SM.
+    const bool tc = s->io == SSD_BF16 && s->headdim == 64 && s->dstate == 128 && (s->nheads / s->ngroups) % 2 == 0;
+    p->seg = tc ? ssd::ragged_segment(tokens, s->nheads / 2, 128, 2 * 148) : ssd::ragged_segment(tokens, s->nheads, 64, 4 * 148);
     p->units = (int)(tokens / p->seg) + nseq;
     // sequences no longer than a segment need no states between launches
     const size_t n = tokens > p->seg ? (size_t)p->units * s->nheads : 0;
@@ -937,7 +938,9 @@ ssd_status ssd_scan_ragged(const ssd_ragged_shape *shape, const ssd_packed *seq,
     a.ws_decay = reinterpret_cast<float *>(ws + plan.decay);
     a.status = static_cast<int *>(workspace);
     a.wait_cycles = wait_cycles_now();
-    cudaError_t e = ssd::launch_ragged_simt(a, shape->io == SSD_BF16, static_cast<cudaStream_t>(stream));
+    const bool bf16 = shape->io == SSD_BF16;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    cudaError_t e = ssd::ragged_tc_supported(a, bf16) ? ssd::launch_ragged_tc(a, cs) : ssd::launch_ragged_simt(a, bf16, cs);
     return e == cudaSuccess ? SSD_OK : cuda_fail(e, "ragged scan launch");
 }
 

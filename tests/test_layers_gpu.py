@@ -232,6 +232,78 @@ def test_scan_ragged_pieces_equal_the_whole(ssd):
         _check(s[0], last[0], tol * lastm[0])
 
 
+# The tensor-core form (bf16, headdim 64, d_state 128, pairs of heads).  One token's y sums, over the
+# tokens before it, C.B scores: P is rounded to bf16 (2^-8) after an exponential of a difference of two
+# sums (their size times u twice: cs below), S is rounded to bf16 where it meets C (2^-8), and y is
+# rounded (2^-8).  With Y the recurrence over absolute values: |dy| <= 2^-8 |y| + (1 + 2^-8) (2^-8 + 2^-12) Y,
+# 2^-12 being room for exponents (|cs| up to 500: 500 u ln 2 times a few) and float32 sums.
+# The state: w x in two bf16 terms is within 2^-17 (a half step of 2^-9 of a rest of at most 2^-8), B exact;
+# w is within (|cs| + 8) 2 u, sums and decays of n / 128 chunks some 3 u each: (2^-17 + 2^-14) S.
+TC = [
+    ([1], 2, 1, 1), ([128], 2, 1, 1), ([127, 129], 4, 2, -1), ([5, 0, 300, 64], 4, 1, 1), ([5, 0, 300, 64], 4, 1, -1),
+    ([700], 2, 1, 1), ([513, 130], 2, 1, -1), ([256, 384], 8, 4, 1), ([1] * 9, 2, 1, 1),
+]
+
+
+def _tc_y(n, N, y, ym):
+    return 2.0 ** -8 * y.abs() + (1 + 2.0 ** -8) * (2.0 ** -8 + 2.0 ** -12) * ym + 1e-37
+
+
+def _tc_s(n, s, sm):
+    return (2.0 ** -17 + 2.0 ** -14) * sm + 1e-37
+
+
+@pytest.mark.parametrize("carry,raw", [(False, False), (True, True)], ids=["zero", "carry"])
+@pytest.mark.parametrize("lens,H,G,direction", TC, ids=str)
+def test_scan_ragged_tensor_core(ssd, lens, H, G, direction, carry, raw):
+    _scan_case(ssd, lens, H, 64, 128, G, "bf16", direction, raw, carry, _tc_y, _tc_s)
+    _scan_case(ssd, lens, H, 64, 128, G, "bf16", direction, raw, carry, _tc_y, _tc_s, skip=False)
+
+
+@pytest.mark.parametrize("direction", [1, -1])
+def test_scan_ragged_tensor_core_steep_and_flat(ssd, direction):
+    """Decays from none at all (A = 0) to hundreds of powers of two within a chunk."""
+    A = torch.tensor([0.0, -0.001, -30.0, -400.0])
+    _scan_case(ssd, [300, 77], 4, 64, 128, 1, "bf16", direction, False, True, _tc_y, _tc_s, A=A)
+
+
+def test_scan_ragged_neighbours_do_not_leak(ssd):
+    """NaN and infinity in one sequence (and behind the last) leave the others bit for bit, states too."""
+    g = _gen("leak")
+    T, H, P, N, lens = 420, 2, 64, 128, [100, 150, 100]
+    _, x, B, C, d, A, D, _ = _scan_inputs(g, T, H, P, N, 1, torch.bfloat16, False)
+    x, B, C, d = (v.contiguous().cuda() for v in (x, B, C, d))
+    for direction in (1, -1):
+        def run():
+            state = torch.zeros(3, H, P, N, device="cuda")
+            y = ssd.ssd_scan_ragged(x, d, A.cuda(), B, C, D.cuda(), cu_seqlens=_cu(lens), direction=direction, state_out=state)
+            return y.clone(), state
+        keep = [v.clone() for v in (x, B, C, d)]
+        y0, s0 = run()
+        for t, r in ((x, 120), (x, 200), (B, 130), (C, 140), (d, 150), (x, 360), (B, 360), (d, 360)):
+            t[r] = float("nan")
+        x[240] = float("inf")
+        y1, s1 = run()
+        for v, k in zip((x, B, C, d), keep):
+            v.copy_(k)
+        assert torch.equal(y0[:100], y1[:100]) and torch.equal(y0[250:350], y1[250:350])
+        assert torch.equal(s0[0], s1[0]) and torch.equal(s0[2], s1[2])
+        assert bool(s1[1].isnan().any())
+
+
+def test_scan_ragged_unaligned_rows_take_the_other_form(ssd):
+    """The tensor-core head shape with rows that a tensor map cannot take: same results within both bounds."""
+    g = _gen("unaligned")
+    T, H = 150, 2
+    wide = torch.randn(T, H * 64 + 2 * 128 + 3, generator=g).to(torch.bfloat16)
+    x, B, C = wide[:, 1:129].unflatten(1, (H, 64)), wide[:, 129:257].unflatten(1, (1, 128)), wide[:, 257:385].unflatten(1, (1, 128))
+    d, A = torch.rand(T, H, generator=g).mul(0.1).to(torch.bfloat16), -torch.ones(H)
+    dev = wide.cuda()
+    xd, Bd, Cd = (dev.as_strided(v.size(), v.stride(), v.storage_offset()) for v in (x, B, C))
+    y = ssd.ssd_scan_ragged(xd, d.cuda(), A.cuda(), Bd, Cd, cu_seqlens=_cu([T]))
+    ref, ym, _, _ = ol.scan(x, d, A, B, C, None, [T])
+    _check(y, ref, 2.0 ** -8 * ref.abs() + 1.01 * (6 * T + 300) * U * ym)
+
 # ---------------------------------------------------------------- single tokens
 
 STEP = [(1, 3, 8, 64, 128, 1, 4, "bf16"), (5, 7, 4, 32, 64, 2, 3, "f32"), (17, 17, 2, 16, 16, 1, 2, "f32"),
