@@ -67,6 +67,8 @@ struct StepArgs {
 };
 cudaError_t launch_step(const StepArgs &a, bool bf16, cudaStream_t st);
 
+constexpr int kRaggedTable = 712;   // floats of a chunk and head's decay table (ragged_tc.cu)
+
 struct RaggedArgs {
     Packed seq;
     Slots slots;                   // float32 pools [n][H][P][N]
@@ -77,6 +79,7 @@ struct RaggedArgs {
     int H, P, N, G, dir;
     int seg, units;                // tokens of a segment, segments at most
     float *ws_state, *ws_decay;    // [units][H][P][N] and [units][H]
+    float *tables;                 // tensor-core form: [tokens / 128 + nseq][H][kRaggedTable]
     int *status;
     long long wait_cycles;
 };

@@ -2,30 +2,48 @@
 // d_state 128, an even number of heads in a B/C group.
 //
 // A CTA walks one segment (ragged.cu) of one sequence for two heads of a group, in chunks of 128
-// tokens.  In the chunk's scan order, with cs_i the inclusive sum of dt A and c = cs of the last token:
+// tokens.  In the chunk's scan order, with cs_i the inclusive sum of dt A, c = cs of the last token and
+// m a reference of the head and chunk:
 //
-//   scores    = C B^T                                              both heads share them
-//   P_ij      = scores_ij exp(cs_i - cs_j) dt_j,  j not after i     (one ex2 per element: cs_j and
-//               dt_j are one number csd_j = cs_j - log2 dt_j, so the exponent never needs a rescue,
-//               however steep the decay is)
-//   y_i       = (P X)_i + exp(cs_i) C_i S^T + D x_i
-//   S        <- exp(c) S + sum_j (w_j x_j) (outer) B_j,             w_j = dt_j exp(c - cs_j)
+//   scores    = C B^T, masked to j not after i                     both heads share them
+//   w_j       = dt_j exp(m - cs_j),  rho_i = exp(cs_i - m)
+//   y_i       = rho_i (scores (w x))_i + exp(cs_i) C_i S^T + D x_i
+//   S        <- exp(c) S + exp(c - m) sum_j (w_j x_j) (outer) B_j
 //
-// Precision.  P and the copy of S that multiplies C are rounded to bf16 (operands of products whose
-// result is a bf16 y).  S itself is a float32 output, so w x enters its product in two bf16 terms,
-// high and rest: 2^-17 of w x instead of 2^-9.  S stays in registers in float32.
+// With m = c / 2 the exponents of w and rho stay within half the chunk's decay: no factor of the decay
+// touches an element of the scores, which are rounded to bf16 as they are and serve both heads.  A
+// chunk that decays by more than 2^150 for one of the two heads takes the long form for both: m = c
+// (no exponent of w is positive), P = scores times the decay, formed for each head, and x as it is in
+// the place of w x.
 //
-// Products (M = 128 each, float32 in TMEM), issued by warp 17 (one elected lane):
+// Precision.  The scores (or P), w x in their product and the copy of S that multiplies C are rounded
+// to bf16 (operands of products whose result is a bf16 y).  S itself is a float32 output, so w x
+// enters its product in two bf16 terms, high and rest: 2^-17 of w x instead of 2^-9.  S stays in
+// registers in float32.
+//
+// Products (M = 128 each, float32 in TMEM):
 //   scores [0,128)     A = C, B = B tile, both K-major in smem
-//   P X    [256,384)   A = P of a head (bf16, TMEM [0,64) and [64,128), written over the scores),
-//                      B = X of the head (MN-major), N = 64 per head
+//   P X    [256,384)   A = P (bf16, in TMEM over the scores: 32 columns of scores become 16 of P, or in
+//                      the long form 16 of each head's, so a warp overwrites only what it has read),
+//                      B = high of w x (MN-major), N = 128; long form: B = x of a head, N = 64 each
 //   C S^T  [384,512)   A = C, B = bf16 S of both heads (MN-major: row n, 128 columns (head, p))
 //   new S  [128,256)   A = B^T (MN-major, M = n), B = w x high, then rest (MN-major), N = 128
 //
-// Warps: 0-15 the passes over tiles (TMEM lane quarter w & 3, column group w >> 2: head w >> 3, half
-// of P), 16 the TMA loads, 17 the MMAs, 18 the y stores.  Per chunk j the passes are: P_j; the state
-// (S <- ... and its bf16 copy for chunk j + 1); w x and the decay tables of chunk j + 1; y_j.  The
-// products of j + 1 that need no state run while y_j is finished.
+// The long form's P.  It is cut into 32 x 32 blocks; with b the last token before row block I,
+// exp(cs_i - cs_j) dt_j = r_i q_j, r_i = exp(cs_i - cs_b), q_j = exp(cs_b - cs_j) dt_j.  P holds scores_ij q_j,
+// and r_i takes the place of rho_i.  q grows past dt only in the diagonal block, by at most the decay
+// of its 32 tokens: a row block that decays by more than 2^60 has r = 1 for its rows, its diagonal
+// block's elements formed one by one, exp(cs_i - cs_j + log dt_j), and r_i q_j multiplied out elsewhere.
+// k_ragged_tables forms the factors of every chunk and head beforehand, so the walk spends nothing on
+// sums along tokens.
+//
+// Warps: 0-7 make P and y, 8-15 the state and w x (TMEM lane quarter w & 3; w >> 2 & 1: two of P's four
+// column blocks, or the head), 16 the TMA loads, 17 to 19 the MMAs: an MMA of N = 128 runs for 32 cycles
+// but takes a thread some 100 to issue, so one issuing warp for the 48 of a chunk would bound it.
+// The two groups run at their own pace.  Group one: P_j, then y_j.  Group two: S from the product of
+// chunk j, w x of chunk j + 1, the bf16 copy of S for chunk j + 1.  Registers: a state warp holds 64
+// columns of S, so the groups are given 88 and 120 a thread and the last warpgroup 56
+// (128 (2 x 88 + 2 x 120 + 56) = 60416 of the 61440 launched with).
 //
 // Rows past the segment's end (another sequence's, or none) are zeroed in x and B before a product
 // sees them, so nothing of theirs, NaN included, enters; their y rows are not written.
@@ -47,21 +65,28 @@ namespace {
 
 constexpr int kQ = 128;                                // tokens of a chunk
 constexpr uint32_t kBox = 128 * 128;                   // 128 rows of 64 bf16: 16 KB
-constexpr int kPassWarps = 16, kTcThreads = 32 * (kPassWarps + 3);
+constexpr int kGroup = 8;                              // warps of a group
+
 // shared memory: everything but the tables in 16 KB boxes; 227 KB in all
 constexpr uint32_t kSX = 0;                            // x: two stages of two heads; becomes y
 constexpr uint32_t kSW = 4 * kBox;                     // w x: high of two heads, rest of two heads
 constexpr uint32_t kSB = 8 * kBox, kSC = 10 * kBox;    // B, C: two 64-column boxes each
 constexpr uint32_t kSS = 12 * kBox;                    // bf16 S: rows n, a box per head
-constexpr uint32_t kTab = 14 * kBox;                   // cs, csd: [2][128] float each
-constexpr uint32_t kBars = kTab + 4 * kQ * 4;
+// One chunk and head's table: the column factors, which every warp reads (copied to shared memory):
+// q of the diagonal blocks, then of row blocks 1, 2, 3 (32, 64 and 96 columns); cs_b of the row blocks,
+// the chunk's decay, the steep blocks' bits,
+// m, and whether the pair takes the short form.  Then per-row values.
+constexpr int kTabQd = 0, kTabQ = 128, kTabRef = 320, kTabTot = 324, kTabSteep = 325, kTabM = 326, kTabShort = 327, kTabShared = 328;
+constexpr int kTabCs = 328, kTabW = 456, kTabCsd = 584, kTabLen = 712;
+constexpr float kSteepBlock = 60.f, kSteepChunk = 150.f;
+static_assert(kTabLen == kRaggedTable, "");
+constexpr uint32_t kTab = 14 * kBox;                   // q of both heads
+constexpr uint32_t kBars = kTab + 2 * kTabShared * 4;
 enum TcBar {
-    XF0 = 0, XF1, XE0, XE1, BF, BE, CF, CE,            // loads: full / empty
-    PREP,                                              // chunk's w x and tables written
+    XF0 = 0, XF1, XE0, XE1, BF, BE, CF, CE, TF,        // loads: full / empty; the tables
+    PREP,                                              // chunk's w x written
     SC, ST, YI, YF,                                    // products done: scores, new S, C S^T, P X
-    RD0, RD1, RD2, RD3,                                // a lane quarter's scores are in registers
     PR, SB, YE,                                        // P written; bf16 S written; Y read
-    SG0, SG1,                                          // y staged
     DONE,
     kNumBars
 };
@@ -70,19 +95,134 @@ constexpr uint32_t kTcSmem = kMisc + 32;
 static_assert(kTcSmem <= 232448, "shared memory budget");
 constexpr uint32_t kColS = 128, kColY = 256, kColYI = 384;   // TMEM columns (scores / P at 0)
 
+// Chunk number of the j-th chunk of sequence s: as the segments are numbered (ragged.cu), with chunks
+// for segments.
+__device__ __forceinline__ int chunk_number(const Segment &sg, int seg, int j) { return sg.lo / kQ + sg.s + sg.k * (seg / kQ) + j; }
+
+// The tables of one chunk for 8 heads, a warp to a head.  Sums along the tokens in float32 in log2
+// units, from the first token on (cs) and from the last back (the exponent of w), so that w does not
+// lose the digits of a difference of large sums.
+constexpr int kTabThreads = 256, kTabHeads = kTabThreads / 32;
+__global__ void __launch_bounds__(kTabThreads) k_ragged_tables(const __grid_constant__ RaggedArgs a) {
+    __shared__ float d[kTabHeads][kQ + 1], tots[kTabHeads];
+    const int c = blockIdx.x, g0 = blockIdx.y * kTabHeads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Segment sg = find_segment(a.seq, kQ, c);
+    if (sg.s < 0 || sg.len == 0) return;
+    const int n = min(kQ, sg.len - sg.k * kQ);
+    const int base = a.dir > 0 ? sg.lo + sg.k * kQ : sg.lo + sg.len - (sg.k + 1) * kQ;
+    {
+        const int h = g0 + (threadIdx.x & 7);
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 32 * i + (threadIdx.x >> 3);
+            const bool in = h < a.H && (a.dir > 0 ? r < n : r >= kQ - n);
+            v[i] = in ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.dt)[(long long)(base + r) * a.lddt + h]) : -INFINITY;
+        }
+        const float bias = a.dt_bias && h < a.H ? a.dt_bias[h] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)                    // -inf: no token
+            d[threadIdx.x & 7][32 * i + (threadIdx.x >> 3)] = v[i] == -INFINITY ? 0.f : a.dt_bias ? softplus(v[i] + bias) : v[i];
+    }
+    __syncthreads();
+    {
+        const int i = warp;
+        const float a2 = g0 + i < a.H ? a.A[g0 + i] * 1.4426950408889634f : 0.f;
+        // lane: four tokens in scan order, 4 lane ..
+        float dt[4], s[4], up[4], dn[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            dt[e] = d[i][a.dir > 0 ? 4 * lane + e : kQ - 1 - (4 * lane + e)];
+            s[e] = dt[e] * a2;
+        }
+        up[0] = s[0]; up[1] = up[0] + s[1]; up[2] = up[1] + s[2]; up[3] = up[2] + s[3];
+        dn[3] = 0.f; dn[2] = s[3]; dn[1] = dn[2] + s[2]; dn[0] = dn[1] + s[1];     // tokens behind
+        float iu = up[3], id = dn[0] + s[0];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float x = __shfl_up_sync(0xffffffffu, iu, o), y = __shfl_down_sync(0xffffffffu, id, o);
+            if (lane >= o) iu += x;
+            if (lane + o < 32) id += y;
+        }
+        float eu = __shfl_up_sync(0xffffffffu, iu, 1), ed = __shfl_down_sync(0xffffffffu, id, 1);
+        if (lane == 0) eu = 0.f;
+        if (lane == 31) ed = 0.f;
+        const float tot = __shfl_sync(0xffffffffu, iu, 31);
+        if (lane == 0) tots[i] = tot;
+        __syncthreads();
+        if (g0 + i >= a.H) return;
+        // (H is even, and the pairs begin at even heads)
+        const bool small = -tots[i] <= kSteepChunk && -tots[i ^ 1] <= kSteepChunk;
+        const float m = small ? 0.5f * tot : tot;
+        float *out = a.tables + ((size_t)c * a.H + g0 + i) * kTabLen;
+        float cs[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) cs[e] = eu + up[e];
+        // cs before and at the end of each scan block of 32 (its last lanes: 7, 15, 23, 31)
+        float b[5];
+        b[0] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) b[k + 1] = __shfl_sync(0xffffffffu, cs[3], 8 * k + 7);
+        const int blk = lane >> 3;
+        const float own = blk == 0 ? b[0] : blk == 1 ? b[1] : blk == 2 ? b[2] : b[3];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int k = 4 * lane + e, row = a.dir > 0 ? k : kQ - 1 - k;      // row of the tile
+            out[kTabCs + row] = cs[e];
+            out[kTabCsd + row] = cs[e] - __log2f(dt[e]);
+            // (the long form's exponent is the sum itself, not a difference)
+            out[kTabW + row] = dt[e] * ex2_ftz(small ? m - cs[e] : ed + dn[e]);
+            out[kTabQd + row] = dt[e] * ex2_ftz(own - cs[e]);
+#pragma unroll
+            for (int I = 1; I < 4; ++I)
+                if (blk < I) out[kTabQ + 16 * I * (I - 1) + 32 * blk + (row & 31)] = dt[e] * ex2_ftz(b[I] - cs[e]);
+        }
+        if (lane == 0) {
+            int steep = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                out[kTabRef + k] = b[k];
+                if (b[k] - b[k + 1] > kSteepBlock) steep |= 1 << k;
+            }
+            out[kTabTot] = tot;
+            out[kTabM] = m;
+            out[kTabShort] = small ? 1.f : 0.f;
+            out[kTabSteep] = __int_as_float(steep);
+        }
+    }
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 struct TcMaps {
-    CUtensorMap x, b, c, y;
+    CUtensorMap x, b, c;
 };
 
+// One lane of a converged warp.  A whole run of MMAs is issued inside one such branch.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
+template <int R> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+constexpr int kTcThreads = 640, kStThreads = 384;      // STATES has no first group of warps
+
 template <bool STATES>
-__global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_constant__ TcMaps maps,
+__global__ void __launch_bounds__(STATES ? kStThreads : kTcThreads, 1) k_ragged_tc(const __grid_constant__ TcMaps maps,
                                                              const __grid_constant__ RaggedArgs a) {
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sbase = smem_u32(sm);
     auto bar = [&](int i) { return sbase + kBars + 8u * i; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + kMisc + 4);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = (threadIdx.x >> 5) + (STATES ? kGroup : 0), lane = threadIdx.x & 31;
     const uint32_t MASK = 0xffffffffu;
     const int pairs = a.H / 2, u = blockIdx.x / pairs, h0 = 2 * (blockIdx.x % pairs), grp = h0 / (a.H / a.G);
     const Segment sg = find_segment(a.seq, a.seg, u);
@@ -98,13 +238,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
     // row of packed token that is row 0 of chunk j's tiles; rows [v0(j), v1(j)) are the segment's
     auto base = [&](int j) { return a.dir > 0 ? sg.lo + t0 + j * kQ : sg.lo + sg.len - t0 - (j + 1) * kQ; };
     auto rows = [&](int j) { return min(kQ, len - j * kQ); };
+    const int chunk0 = chunk_number(sg, a.seg, 0);
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         *reinterpret_cast<volatile long long *>(abort_flag + 1) = a.wait_cycles;
         for (int i = 0; i < kNumBars; ++i) {
-            const bool w16 = i == PREP || i == PR || i == SB || i == YE || i == SG0 || i == SG1 || (STATES && (i == XE0 || i == XE1));
-            mbar_init(bar(i), w16 ? kPassWarps : (i >= RD0 && i <= RD3) ? 4 : 1);
+            const bool group = i == PREP || i == PR || i == SB || i == YE || i == XE0 || i == XE1;
+            mbar_init(bar(i), group ? kGroup : i == DONE ? 3 : (i == BE && !STATES) ? 2 : 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -118,11 +259,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
     const uint32_t tmem = *tmem_slot;
     auto wait = [&](int b, int phase, int code) { return mbar_wait(bar(b), (uint32_t)phase & 1, MASK, abort_flag, a.status, code); };
 
+    if (!STATES && warp >= 16) regs_down<56>();
     if (warp == 16) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
             auto wait1 = [&](int b, int phase, int code) { return mbar_wait(bar(b), (uint32_t)phase & 1, 1u, abort_flag, a.status, code); };
-            int nx = 0, nb = 0, ncc = 0;               // chunks asked for
+            int nx = 0, nb = 0, ncc = 0, nt = 0;       // chunks asked for
             for (int j = 0; j < nc; ++j) {
                 const int r = base(j), st = j & 1;
                 if (j >= 2 && !wait1(XE0 + st, (j >> 1) - 1, 151)) break;
@@ -138,89 +280,278 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
                 mbar_expect_tx(bar(CF), 2 * kBox);
                 for (int h = 0; h < 2; ++h) tma_load_2d(sbase + kSC + h * kBox, &maps.c, 128 * grp + 64 * h, r, bar(CF));
                 ncc = j + 1;
+                if (j + 2 < nc) {                      // its loads wait for buffers; from L2 they take half as long
+                    for (int h = 0; h < 2; ++h) tma_prefetch_2d(&maps.x, 64 * (h0 + h), base(j + 2));
+                    for (int h = 0; h < 2; ++h) tma_prefetch_2d(&maps.b, 128 * grp + 64 * h, base(j + 2));
+                    for (int h = 0; h < 2; ++h) tma_prefetch_2d(&maps.c, 128 * grp + 64 * h, base(j + 2));
+                }
+                // the tables of the chunk before are read by its P pass
+                if (j >= 1 && !wait1(PR, j - 1, 162)) break;
+                mbar_expect_tx(bar(TF), 2 * kTabShared * 4);
+                for (int h = 0; h < 2; ++h)
+                    bulk_load(sbase + kTab + h * kTabShared * 4, a.tables + ((size_t)(chunk0 + j) * a.H + h0 + h) * kTabLen,
+                              kTabShared * 4, bar(TF));
+                nt = j + 1;
             }
             if (*abort_flag) {                         // copies in flight land before the memory is given up
                 for (int j = nx - 1; j >= 0 && j >= nx - 2; --j) mbar_drain(bar(XF0 + (j & 1)), (uint32_t)(j >> 1) & 1, a.wait_cycles);
                 if (nb) mbar_drain(bar(BF), (uint32_t)(nb - 1) & 1, a.wait_cycles);
                 if (ncc) mbar_drain(bar(CF), (uint32_t)(ncc - 1) & 1, a.wait_cycles);
+                if (nt) mbar_drain(bar(TF), (uint32_t)(nt - 1) & 1, a.wait_cycles);
             }
         }
         __syncwarp();
     } else if (warp == 17) {
-        // ------------------------------------------------------------ products
-        const uint32_t id_sc = idesc(128, 0, 0), id_px = idesc(64, 0, 1), id_yi = idesc(128, 0, 1), id_st = idesc(128, 1, 1);
-        const SDesc dC = make_sdesc(sbase + kSC, 16, 1024), dBk = make_sdesc(sbase + kSB, 16, 1024);
-        const SDesc dBm = make_sdesc(sbase + kSB, kBox, 1024), dW = make_sdesc(sbase + kSW, kBox, 1024),
-                    dS = make_sdesc(sbase + kSS, kBox, 1024);
-        for (int j = 0; j < nc; ++j) {
-            if (!wait(PREP, j, 154) || !wait(BF, j, 155) || !wait(XF0 + (j & 1), j >> 1, 156)) break;
-            if (!STATES) {
-                if (!wait(CF, j, 157)) break;
+        // ------------------------------------------------------------ products that read C: scores, C S^T
+        if (!STATES) {
+            const uint32_t id_sc = idesc(128, 0, 0), id_yi = idesc(128, 0, 1);
+            const SDesc dC = make_sdesc(sbase + kSC, 16, 1024), dBk = make_sdesc(sbase + kSB, 16, 1024), dS = make_sdesc(sbase + kSS, kBox, 1024);
+            for (int j = 0; j < nc; ++j) {
+                // P of the chunk before lies over the scores until P X has read it; a partial chunk's B
+                // is zeroed in part first
+                if (!wait(BF, j, 155) || !wait(CF, j, 157) || (j >= 1 && !wait(YF, j - 1, 156)) || (rows(j) < kQ && !wait(PREP, j, 154)))
+                    break;
                 tc_fence_after();
                 // K = n: 64 of them to a box, 16 to a step of 32 bytes
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint32_t off = (ks >> 2) * kBox + (ks & 3) * 32;
-                    mma_ss_w(tmem, dC.at(off), dBk.at(off), id_sc, ks > 0);
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const uint32_t off = (ks >> 2) * kBox + (ks & 3) * 32;
+                        mma_ss(tmem, dC.at(off), dBk.at(off), id_sc, ks > 0);
+                    }
+                    mma_commit(bar(SC));
+                    mma_commit(bar(BE));
                 }
-                mma_commit_w(bar(SC));
+                __syncwarp();
+                if (!wait(SB, j, 158) || (j >= 1 && !wait(YE, j - 1, 159))) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ss(tmem + kColYI, dC.at((ks >> 2) * kBox + (ks & 3) * 32), dS.at(ks * 2048), id_yi, ks > 0);
+                    mma_commit(bar(YI));
+                    mma_commit(bar(CE));
+                }
+                __syncwarp();
             }
-            tc_fence_after();
-            // K = tokens: 16 rows of 128 bytes to a step
-#pragma unroll
-            for (int ks = 0; ks < 16; ++ks)
-                mma_ss_w(tmem + kColS, dBm.at((ks & 7) * 2048), dW.at((ks >> 3) * 2 * kBox + (ks & 7) * 2048), id_st, ks > 0);
-            mma_commit_w(bar(ST));
-            mma_commit_w(bar(BE));
-            if (STATES) continue;
-            if (!wait(SB, j, 158) || (j >= 1 && !wait(YE, j - 1, 159))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                mma_ss_w(tmem + kColYI, dC.at((ks >> 2) * kBox + (ks & 3) * 32), dS.at(ks * 2048), id_yi, ks > 0);
-            mma_commit_w(bar(YI));
-            mma_commit_w(bar(CE));
-            if (!wait(PR, j, 160)) break;
-            tc_fence_after();
-            const SDesc dX = make_sdesc(sbase + kSX + (j & 1) * 2 * kBox, kBox, 1024);
-#pragma unroll
-            for (int ks = 0; ks < 16; ++ks)
-                mma_ts_w(tmem + kColY + 64 * (ks >> 3), tmem + 64 * (ks >> 3) + 8 * (ks & 7), dX.at((ks >> 3) * kBox + (ks & 7) * 2048),
-                         id_px, (ks & 7) > 0);
-            mma_commit_w(bar(YF));
         }
-        mma_commit_w(bar(DONE));
+        if (elect_one()) mma_commit(bar(DONE));
         if (lane == 0) mbar_drain(bar(DONE), 0, a.wait_cycles);
         __syncwarp();
     } else if (warp == 18) {
-        // ------------------------------------------------------------ y stores (whole chunks; a partial one is stored by the passes)
-        if (!STATES && lane == 0) {
+        // ------------------------------------------------------------ the product of the state (K = tokens: 16 rows of 128 bytes to a step)
+        const uint32_t id_st = idesc(128, 1, 1);
+        const SDesc dBm = make_sdesc(sbase + kSB, kBox, 1024), dW = make_sdesc(sbase + kSW, kBox, 1024);
+        for (int j = 0; j < nc; ++j) {
+            if (!wait(PREP, j, 160) || !wait(BF, j, 172)) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 16; ++ks)
+                    mma_ss(tmem + kColS, dBm.at((ks & 7) * 2048), dW.at((ks >> 3) * 2 * kBox + (ks & 7) * 2048), id_st, ks > 0);
+                mma_commit(bar(ST));
+                mma_commit(bar(BE));
+            }
+            __syncwarp();
+        }
+        if (elect_one()) mma_commit(bar(DONE));
+        if (lane == 0) mbar_drain(bar(DONE), 0, a.wait_cycles);
+        __syncwarp();
+    } else if (warp == 19) {
+        // ------------------------------------------------------------ P X
+        if (!STATES) {
+            const uint32_t id_px = idesc(64, 0, 1), id_pw = idesc(128, 0, 1);
+            const SDesc dW = make_sdesc(sbase + kSW, kBox, 1024);
+            const float *tg = a.tables + ((size_t)chunk0 * a.H + h0) * kTabLen + kTabShort;
+            float next = nc > 0 ? *tg : 0.f;
+            const SDesc dX0 = make_sdesc(sbase + kSX, kBox, 1024), dX1 = make_sdesc(sbase + kSX + 2 * kBox, kBox, 1024);
+            for (int j = 0; j < nc; ++j) {
+                const bool small = next != 0.f;
+                tg += (size_t)a.H * kTabLen;
+                if (j + 1 < nc) next = *tg;
+                if (!wait(XF0 + (j & 1), j >> 1, 173) || !wait(PREP, j, 174) || !wait(PR, j, 175)) break;
+                tc_fence_after();
+                const SDesc dX = j & 1 ? dX1 : dX0;
+                if (small) {
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_ts(tmem + kColY, tmem + 32 * (ks >> 1) + 8 * (ks & 1), dW.at(ks * 2048), id_pw, ks > 0);
+                        mma_commit(bar(YF));
+                    }
+                } else if (elect_one()) {
+#pragma unroll
+                    for (int ks = 0; ks < 16; ++ks)
+                        mma_ts(tmem + kColY + 64 * (ks >> 3), tmem + 32 * (ks >> 1 & 3) + 16 * (ks >> 3) + 8 * (ks & 1),
+                               dX.at((ks >> 3) * kBox + (ks & 7) * 2048), id_px, (ks & 7) > 0);
+                    mma_commit(bar(YF));
+                }
+                __syncwarp();
+            }
+        }
+        if (elect_one()) mma_commit(bar(DONE));
+        if (lane == 0) mbar_drain(bar(DONE), 0, a.wait_cycles);
+        __syncwarp();
+    } else if (warp < kGroup) {
+        // ------------------------------------------------------------ P and y
+        if constexpr (!STATES) {
+            regs_down<88>();
+            const int q = warp & 3, hh = warp >> 2, h = h0 + hh, row = 32 * q + lane;
+            const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
+            const float *tab = reinterpret_cast<const float *>(sm + kTab);
+            const float Dh = a.D ? a.D[h] : 0.f;
+            const int rb = a.dir > 0 ? q : 3 - q;      // scan number of the row block
+            const float *tg = a.tables + ((size_t)chunk0 * a.H + h0) * kTabLen;   // chunk j's: j a.H kTabLen on
+            float n0 = 0.f, n1 = 0.f;                  // cs of the row and both heads, loaded a chunk ahead
+            if (nc > 0) {
+                n0 = tg[kTabCs + row];
+                n1 = tg[kTabLen + kTabCs + row];
+            }
             for (int j = 0; j < nc; ++j) {
                 const int st = j & 1;
-                if (!mbar_wait(bar(SG0 + st), (uint32_t)(j >> 1) & 1, 1u, abort_flag, a.status, 161)) break;
-                if (rows(j) == kQ) {
-                    for (int h = 0; h < 2; ++h) tma_store_2d(&maps.y, sbase + kSX + (2 * st + h) * kBox, 64 * (h0 + h), base(j));
-                    bulk_commit();
-                    bulk_wait_read0();
+                const float cs0 = n0, cs1 = n1;
+                const float *t0p = tg, *t1p = tg + kTabLen;
+                tg += (size_t)a.H * kTabLen;
+                if (j + 1 < nc) {
+                    n0 = tg[kTabCs + row];
+                    n1 = tg[kTabLen + kTabCs + row];
                 }
-                mbar_arrive(bar(XE0 + st));
+                if (!wait(TF, j, 165)) break;
+                const float *u0 = tab, *u1 = tab + kTabShared;
+                const bool small = u0[kTabShort] != 0.f;
+                const float rf0 = ex2_ftz(cs0 - u0[kTabRef + rb]), rf1 = ex2_ftz(cs1 - u1[kTabRef + rb]);
+                const bool steep0 = __float_as_int(u0[kTabSteep]) >> rb & 1, steep1 = __float_as_int(u1[kTabSteep]) >> rb & 1;
+                const float ecs = ex2_ftz(hh ? cs1 : cs0), ry = small ? ex2_ftz(hh ? cs1 - u1[kTabM] : cs0 - u0[kTabM]) : hh ? (steep1 ? 1.f : rf1) : (steep0 ? 1.f : rf0);
+                // ---- P_j: this thread's row, column blocks 2 hh and 2 hh + 1
+                if (!wait(SC, j, 166)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x) {
+                    const int cg = 2 * hh + x, cb = a.dir > 0 ? cg : 3 - cg;
+                    if (cb > rb) {
+                        const uint32_t zero[16] = {};
+                        tmem_st16_nw(tl + 32 * cg, zero);
+                        if (!small) tmem_st16_nw(tl + 32 * cg + 16, zero);
+                        continue;
+                    }
+                    const bool diag = cb == rb;
+                    float v[32];
+                    tmem_ld32(tl + 32 * cg, v);
+                    // columns of a diagonal block that are not after its row
+                    if (diag) {
+                        if (a.dir > 0)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = i <= lane ? v[i] : 0.f;
+                        else
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = i >= lane ? v[i] : 0.f;
+                    }
+                    if (small) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) p[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+                        tmem_st16_nw(tl + 32 * cg, p);
+                        continue;
+                    }
+#pragma unroll 1
+                    for (int z = 0; z < 2; ++z) {
+                        uint32_t p[16];
+                        const bool steep = z ? steep1 : steep0;
+                        if (!(diag && steep)) {
+                            const float4 *qt = reinterpret_cast<const float4 *>(
+                                tab + z * kTabShared + (diag ? kTabQd + 32 * cg : kTabQ + 16 * rb * (rb - 1) + 32 * cb));
+                            if (steep) {
+                                const float r = z ? rf1 : rf0;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float4 e = qt[i];
+                                    p[2 * i] = pack_bf16(v[4 * i] * r * e.x, v[4 * i + 1] * r * e.y);
+                                    p[2 * i + 1] = pack_bf16(v[4 * i + 2] * r * e.z, v[4 * i + 3] * r * e.w);
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float4 e = qt[i];
+                                    const float2 lo = mul2(make_float2(v[4 * i], v[4 * i + 1]), make_float2(e.x, e.y));
+                                    const float2 hi = mul2(make_float2(v[4 * i + 2], v[4 * i + 3]), make_float2(e.z, e.w));
+                                    p[2 * i] = pack_bf16(lo.x, lo.y);
+                                    p[2 * i + 1] = pack_bf16(hi.x, hi.y);
+                                }
+                            }
+                        } else {
+                            // (a column past the row has a positive exponent, of any size: no product with it)
+                            const float *ct = (z ? t1p : t0p) + kTabCsd + 32 * cg, c = z ? cs1 : cs0;
+                            auto el = [&](int i) {
+                                const bool in = a.dir > 0 ? i <= lane : i >= lane;
+                                return in ? v[i] * ex2_ftz(c - ct[i]) : 0.f;
+                            };
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) p[i] = pack_bf16(el(2 * i), el(2 * i + 1));
+                        }
+                        // in place: the block's 32 score columns become 16 of each head
+                        tmem_st16_nw(tl + 32 * cg + 16 * z, p);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(PR));
+                // ---- y_j, in place over x_j: this thread's row of head h
+                if (!wait(YI, j, 170) || !wait(YF, j, 171)) break;
+                tc_fence_after();
+                uint8_t *box = sm + kSX + (2 * st + hh) * kBox;
+                const float2 e2 = make_float2(ecs, ecs), d2 = make_float2(Dh, Dh), r2 = make_float2(ry, ry);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    float yp[16], yi[16];
+                    tmem_ld16(tl + kColY + 64 * hh + 16 * z, yp);
+                    tmem_ld16(tl + kColYI + 64 * hh + 16 * z, yi);
+                    if (z == 3) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(YE));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint4 *at = reinterpret_cast<uint4 *>(box + swz(row, 2 * z + i));
+                        const uint4 x = *at;
+                        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                        uint32_t o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int c = 8 * i + 2 * e;
+                            const float2 t = fma2(e2, make_float2(yi[c], yi[c + 1]), mul2(d2, unpack2(in[e])));
+                            const float2 y2 = fma2(r2, make_float2(yp[c], yp[c + 1]), t);
+                            o[e] = pack_bf16(y2.x, y2.y);
+                        }
+                        *at = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                }
+                // the warp's 32 rows x 128 bytes, eight lanes to a row, rows of the segment only
+                __syncwarp();
+                const int n = rows(j);
+                uint4 o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = *reinterpret_cast<const uint4 *>(box + swz(32 * q + 4 * i + (lane >> 3), lane & 7));
+                fence_async_smem();                    // the next load of this stage comes after these accesses
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(XE0 + st));
+                __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + (long long)(base(j) + 32 * q + (lane >> 3)) * a.ldy + h * 64 + 8 * (lane & 7);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 32 * q + 4 * i + (lane >> 3);
+                    if (a.dir > 0 ? r < n : r >= kQ - n) __stcs(reinterpret_cast<uint4 *>(y + 4LL * i * a.ldy), o[i]);
+                }
             }
-            bulk_wait0();
         }
-        __syncwarp();
-    } else {
-        // ------------------------------------------------------------ passes
-        const int q = warp & 3, cg = warp >> 2, hh = cg >> 1, half = cg & 1, h = h0 + hh;
-        const int row = 32 * q + lane;                 // token row of a tile, or n of the state
+    } else if (warp < 2 * kGroup) {
+        // ------------------------------------------------------------ the state and w x
+        if constexpr (!STATES) regs_up<120>();
+        const int q = warp & 3, hh = warp >> 2 & 1, h = h0 + hh, row = 32 * q + lane;   // n of the state, row of w x
         const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
-        float *cs_tab = reinterpret_cast<float *>(sm + kTab), *csd_tab = cs_tab + 2 * kQ;
-        const float a2 = a.A[h] * 1.4426950408889634f, Dh = a.D ? a.D[h] : 0.f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
-        const __nv_bfloat16 *dtp = static_cast<const __nv_bfloat16 *>(a.dt) + h;
-        const size_t PN = 64 * 128;
-        float S[32];                                   // S[h][32 half + i][row]
-        // ---- start state
+        const size_t PN = 64 * 128, at = (size_t)h * PN + row;
+        float S[64];                                   // S[h][i][row]
         {
-            const size_t at = (size_t)h * PN + (size_t)(32 * half) * 128 + row;
             const float *in = nullptr;
             if (sg.k == 0) {
                 if (STATES || last) {
@@ -233,12 +564,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
                 in = a.ws_state + (size_t)(u - sg.k) * a.H * PN;
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) S[i] = in ? in[at + i * 128] : 0.f;
+            for (int i = 0; i < 64; ++i) S[i] = in ? in[at + i * 128] : 0.f;
             if (STATES && sg.k == 0) {
                 // the sequence's start, kept where its last segment's own state would be (nothing reads that)
                 float *keep = a.ws_state + (size_t)(u + sg.count - 1) * a.H * PN;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) keep[at + i * 128] = S[i];
+                for (int i = 0; i < 64; ++i) keep[at + i * 128] = S[i];
             }
             if (!STATES)
                 for (int k = 1; k < sg.k; ++k) {
@@ -246,99 +577,54 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
                     const float d = ex2_ftz(a.ws_decay[v + h]);
                     const float *add = a.ws_state + v * PN + at;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) S[i] = fmaf(S[i], d, add[i * 128]);
+                    for (int i = 0; i < 64; ++i) S[i] = fmaf(S[i], d, add[i * 128]);
                 }
         }
-        auto copy_state = [&]() {                      // bf16 S: row n, 32 columns of the head's box
+        auto copy_state = [&]() {                      // bf16 S: row n of the head's box
             uint8_t *box = sm + kSS + hh * kBox;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4 *>(box + swz(row, 4 * half + i)) =
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4 *>(box + swz(row, i)) =
                     make_uint4(pack_bf16(S[8 * i], S[8 * i + 1]), pack_bf16(S[8 * i + 2], S[8 * i + 3]),
                                pack_bf16(S[8 * i + 4], S[8 * i + 5]), pack_bf16(S[8 * i + 6], S[8 * i + 7]));
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(SB));
         };
-        float dtr[4], kappa = 1.f, total = 0.f;        // dt of rows 4 lane ..; decay of the present chunk; of the segment (log2)
-        auto load_dt = [&](int j) {
-            const int b = base(j), n = rows(j);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = 4 * lane + e;
-                const bool in = a.dir > 0 ? r < n : r >= kQ - n;
-                dtr[e] = in ? __bfloat162float(dtp[(long long)(b + r) * a.lddt]) : -INFINITY;   // -inf: no token
-            }
+        float wr = 0.f, tot = 0.f, ref = 0.f, total = 0.f;   // w of this row, c and m (log2) of the chunk prepared last
+        auto load_w = [&](int j) {
+            const float *t = a.tables + ((size_t)(chunk0 + j) * a.H + h) * kTabLen;
+            wr = t[kTabW + row];
+            tot = t[kTabTot];
+            ref = t[kTabM];
         };
-        // tables and w x of chunk j, from dtr
-        float next_kappa = 1.f;
+        // w x of chunk j
         auto prepare = [&](int j) -> bool {
             const int st = j & 1, n = rows(j);
-            float d[4], s[4], up[4], dn[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                d[e] = dtr[e] == -INFINITY ? 0.f : (a.dt_bias ? softplus(dtr[e] + bias) : dtr[e]);
-                s[e] = d[e] * a2;
-            }
-            // inclusive sums from the first row on and from the last row back
-            up[0] = s[0]; up[1] = up[0] + s[1]; up[2] = up[1] + s[2]; up[3] = up[2] + s[3];
-            dn[3] = s[3]; dn[2] = dn[3] + s[2]; dn[1] = dn[2] + s[1]; dn[0] = dn[1] + s[0];
-            float iu = up[3], id = dn[0];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float x = __shfl_up_sync(MASK, iu, o), y = __shfl_down_sync(MASK, id, o);
-                if (lane >= o) iu += x;
-                if (lane + o < 32) id += y;
-            }
-            const float tot = __shfl_sync(MASK, iu, 31);
-            float eu = __shfl_up_sync(MASK, iu, 1), ed = __shfl_down_sync(MASK, id, 1);
-            if (lane == 0) eu = 0.f;
-            if (lane == 31) ed = 0.f;
-            float cs[4], wv[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float tail = a.dir > 0 ? ed + (e < 3 ? dn[e < 3 ? e + 1 : 3] : 0.f) : eu + (e > 0 ? up[e > 0 ? e - 1 : 0] : 0.f);
-                cs[e] = a.dir > 0 ? eu + up[e] : ed + dn[e];
-                wv[e] = d[e] * ex2_ftz(tail);
-            }
-            next_kappa = ex2_ftz(tot);
-            total += tot;
-            if (!STATES && q == 0 && half == 0) {
-                // the tables of the chunk before are read by the P pass: wait until all of it is over
-                if (j >= 1 && !wait(PR, j - 1, 162)) return false;
-                reinterpret_cast<float4 *>(cs_tab + hh * kQ)[lane] = make_float4(cs[0], cs[1], cs[2], cs[3]);
-                reinterpret_cast<float4 *>(csd_tab + hh * kQ)[lane] =
-                    make_float4(cs[0] - __log2f(d[0]), cs[1] - __log2f(d[1]), cs[2] - __log2f(d[2]), cs[3] - __log2f(d[3]));
-            }
-            // w of this thread's row: element lane & 3 of lane 8 q + lane / 4
-            float wr = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float t = __shfl_sync(MASK, wv[e], 8 * q + (lane >> 2));
-                if ((lane & 3) == e) wr = t;
-            }
             if (!wait(XF0 + st, j >> 1, 163)) return false;
-            const bool mine = a.dir > 0 ? row < n : row >= kQ - n;
+            uint8_t *x = sm + kSX + (2 * st + hh) * kBox;
             if (n < kQ) {                              // rows of no token: zero in x and B
                 if (!wait(BF, j, 164)) return false;
-                if (!mine)
+                if (a.dir > 0 ? row >= n : row < kQ - n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        *reinterpret_cast<uint4 *>(sm + kSX + (2 * st + hh) * kBox + swz(row, 4 * half + i)) = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4 *>(sm + kSB + hh * kBox + swz(row, 4 * half + i)) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int i = 0; i < 8; ++i) {
+                        *reinterpret_cast<uint4 *>(x + swz(row, i)) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(sm + kSB + hh * kBox + swz(row, i)) = make_uint4(0u, 0u, 0u, 0u);
                     }
             }
+            const float2 w2 = make_float2(wr, wr), m1 = make_float2(-1.f, -1.f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t off = swz(row, 4 * half + i);
-                const uint4 v = *reinterpret_cast<const uint4 *>(sm + kSX + (2 * st + hh) * kBox + off);
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t off = swz(row, i);
+                const uint4 v = *reinterpret_cast<const uint4 *>(x + off);
                 const uint32_t in[4] = {v.x, v.y, v.z, v.w};
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 f = mul2(unpack2(in[e]), make_float2(wr, wr));
+                    const float2 f = mul2(unpack2(in[e]), w2);
                     hi[e] = pack_bf16(f.x, f.y);
-                    lo[e] = pack_bf16(f.x - bf16lo(hi[e]), f.y - bf16hi(hi[e]));
+                    const float2 rest = fma2(unpack2(hi[e]), m1, f);
+                    lo[e] = pack_bf16(rest.x, rest.y);
                 }
                 *reinterpret_cast<uint4 *>(sm + kSW + hh * kBox + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4 *>(sm + kSW + (2 + hh) * kBox + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -351,129 +637,45 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
             }
             return true;
         };
-
         bool ok = true;
         if (nc > 0) {
-            load_dt(0);
+            load_w(0);
             if (!STATES) copy_state();
             ok = prepare(0);
         }
         for (int j = 0; j < nc && ok; ++j) {
-            const int st = j & 1;
-            kappa = next_kappa;
-            if (j + 1 < nc) load_dt(j + 1);
-            float ecs = 0.f;
-            if (!STATES) {
-                // ---- P_j: this thread's row, columns [32 cg, 32 cg + 32)
-                if (!(ok = wait(PREP, j, 165) && wait(SC, j, 166))) break;
-                tc_fence_after();
-                const bool diag = cg == q, live = a.dir > 0 ? cg <= q : cg >= q;
-                float v[32];
-                if (live) tmem_ld32(tl + 32 * cg, v);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(RD0 + q));
-                // P goes over the scores once the quarter's four warps have them in registers
-                if (!(ok = wait(RD0 + q, j, 167))) break;
-                tc_fence_after();
-                ecs = ex2_ftz(cs_tab[hh * kQ + row]);
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                    uint32_t p[16];
-                    const float c = cs_tab[z * kQ + row];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 e = *reinterpret_cast<const float4 *>(csd_tab + z * kQ + 32 * cg + 4 * i);
-                        const float m0 = v[4 * i] * ex2_ftz(c - e.x), m1 = v[4 * i + 1] * ex2_ftz(c - e.y),
-                                    m2 = v[4 * i + 2] * ex2_ftz(c - e.z), m3 = v[4 * i + 3] * ex2_ftz(c - e.w);
-                        p[2 * i] = live ? pack_bf16(m0, m1) : 0u;
-                        p[2 * i + 1] = live ? pack_bf16(m2, m3) : 0u;
-                    }
-                    if (diag)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            // columns 2 i and 2 i + 1 of the quarter against row `lane` of it
-                            const bool k0 = a.dir > 0 ? 2 * i <= lane : 2 * i >= lane, k1 = a.dir > 0 ? 2 * i + 1 <= lane : 2 * i + 1 >= lane;
-                            p[i] &= (k0 ? 0x0000ffffu : 0u) | (k1 ? 0xffff0000u : 0u);
-                        }
-                    tmem_st16_nw(tl + 64 * z + 16 * cg, p);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(PR));
-            }
-            // ---- the state
+            const float kappa = ex2_ftz(tot), add = ex2_ftz(tot - ref);
+            total += tot;
+            if (j + 1 < nc) load_w(j + 1);
             if (!(ok = wait(ST, j, 168))) break;
             tc_fence_after();
-            {
+            const float2 k2 = make_float2(kappa, kappa), a2 = make_float2(add, add);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
                 float ds[32];
-                tmem_ld32(tl + kColS + 32 * cg, ds);
+                tmem_ld32(tl + kColS + 64 * hh + 32 * z, ds);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) S[i] = fmaf(S[i], kappa, ds[i]);
+                for (int i = 0; i < 32; i += 2) {
+                    const float2 n2 = fma2(make_float2(S[32 * z + i], S[32 * z + i + 1]), k2, mul2(make_float2(ds[i], ds[i + 1]), a2));
+                    S[32 * z + i] = n2.x;
+                    S[32 * z + i + 1] = n2.y;
+                }
             }
-            if (!STATES && j + 1 < nc) {
-                if (!(ok = wait(YI, j, 169))) break;   // C S^T has read the copy it is written over
-                copy_state();
-            }
-            // ---- the next chunk's w x and tables
             tc_fence_before();
-            if (j + 1 < nc && !(ok = prepare(j + 1))) break;
-            if (!STATES) {
-                // ---- y_j, in place over x_j
-                if (!(ok = wait(YI, j, 170) && wait(YF, j, 171))) break;
-                tc_fence_after();
-                uint8_t *box = sm + kSX + (2 * st + hh) * kBox;
-#pragma unroll
-                for (int z = 0; z < 2; ++z) {          // 16 columns at a time: more do not fit beside S
-                    float yp[16], yi[16];
-                    tmem_ld16(tl + kColY + 32 * cg + 16 * z, yp);
-                    tmem_ld16(tl + kColYI + 32 * cg + 16 * z, yi);
-                    if (z == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(YE));
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint4 *at = reinterpret_cast<uint4 *>(box + swz(row, 4 * half + 2 * z + i));
-                        const uint4 x = *at;
-                        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-                        uint32_t o[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int c = 8 * i + 2 * e;
-                            o[e] = pack_bf16(fmaf(Dh, bf16lo(in[e]), fmaf(ecs, yi[c], yp[c])),
-                                             fmaf(Dh, bf16hi(in[e]), fmaf(ecs, yi[c + 1], yp[c + 1])));
-                        }
-                        *at = make_uint4(o[0], o[1], o[2], o[3]);
-                    }
+            if (j + 1 < nc) {
+                if (!STATES && !(ok = wait(YF, j, 176))) break;   // P X has read w x
+                if (!(ok = prepare(j + 1))) break;
+                if (!STATES) {
+                    if (!(ok = wait(YI, j, 169))) break;   // C S^T has read the copy it is written over
+                    copy_state();
                 }
-                const int n = rows(j);
-                if (n == kQ) {
-                    fence_async_smem();
-                } else {
-                    // the warp's 32 rows x 64 bytes, four lanes to a row, rows of the segment only
-                    __syncwarp();
-                    __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + (long long)h * 64 + 32 * half;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 32 * q + 8 * i + (lane >> 2), c = lane & 3;
-                        if (a.dir > 0 ? r < n : r >= kQ - n)
-                            *reinterpret_cast<uint4 *>(y + (long long)(base(j) + r) * a.ldy + 8 * c) =
-                                *reinterpret_cast<const uint4 *>(box + swz(r, 4 * half + c));
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(SG0 + st));
             }
         }
-        // ---- end state
         if (ok) {
             float *out = nullptr;
             if (STATES) {
                 out = a.ws_state + (size_t)u * a.H * PN;
-                if (q == 0 && half == 0 && lane == 0) a.ws_decay[(size_t)u * a.H + h] = total;
+                if (q == 0 && lane == 0) a.ws_decay[(size_t)u * a.H + h] = total;
             } else if (last && a.slots.pool_out) {
                 // (slot_of_end meets at a CTA barrier: its look for a second writer is done warp by warp here)
                 const int v = a.slots.out ? a.slots.out[sg.s] : sg.s;
@@ -489,11 +691,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
                 }
                 if (good) out = static_cast<float *>(a.slots.pool_out) + (size_t)v * a.H * PN;
             }
-            if (out) {
-                out += (size_t)h * PN + (size_t)(32 * half) * 128 + row;
+            if (out)
 #pragma unroll
-                for (int i = 0; i < 32; ++i) out[i * 128] = S[i];
-            }
+                for (int i = 0; i < 64; ++i) out[at + i * 128] = S[i];
         }
     }
     tc_fence_before();
@@ -527,15 +727,16 @@ cudaError_t launch_ragged_tc(const RaggedArgs &a, cudaStream_t st) {
     TcMaps m;
     memset(&m, 0, sizeof m);
     const uint64_t T = a.seq.tokens, HP = 64ull * a.H, GN = 128ull * a.G;
-    if (!map_rows(&m.x, a.x, T, HP, a.ldx) || !map_rows(&m.b, a.B, T, GN, a.ldB) || !map_rows(&m.c, a.C, T, GN, a.ldC) ||
-        !map_rows(&m.y, a.y, T, HP, a.ldy))
+    if (!map_rows(&m.x, a.x, T, HP, a.ldx) || !map_rows(&m.b, a.B, T, GN, a.ldB) || !map_rows(&m.c, a.C, T, GN, a.ldC))
         return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)(a.units * (a.H / 2));
-    cudaError_t e;
+    k_ragged_tables<<<dim3(a.seq.tokens / kQ + a.seq.nseq, (a.H + kTabHeads - 1) / kTabHeads), kTabThreads, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     if (a.seq.tokens > a.seg) {
         e = cudaFuncSetAttribute(k_ragged_tc<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
         if (e != cudaSuccess) return e;
-        k_ragged_tc<true><<<grid, kTcThreads, kTcSmem, st>>>(m, a);
+        k_ragged_tc<true><<<grid, kStThreads, kTcSmem, st>>>(m, a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     e = cudaFuncSetAttribute(k_ragged_tc<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);

@@ -837,7 +837,7 @@ ssd_status check_step(const ssd_step_shape *s) {
 
 struct RaggedPlan {
     int seg, units;
-    size_t state, decay, total;     // workspace offsets and size
+    size_t state, decay, tables, total;     // workspace offsets and size
 };
 
 ssd_status ragged_plan(const ssd_ragged_shape *s, long long tokens, int nseq, RaggedPlan *p) {
@@ -853,7 +853,8 @@ ssd_status ragged_plan(const ssd_ragged_shape *s, long long tokens, int nseq, Ra
     const size_t n = tokens > p->seg ? (size_t)p->units * s->nheads : 0;
     p->state = kStatusBytes;
     p->decay = p->state + round_up(n * s->headdim * s->dstate * sizeof(float));
-    p->total = p->decay + round_up(n * sizeof(float));
+    p->tables = p->decay + round_up(n * sizeof(float));
+    p->total = p->tables + (tc ? round_up((size_t)(tokens / 128 + nseq) * s->nheads * ssd::kRaggedTable * sizeof(float)) : 0);
     return SSD_OK;
 }
 
@@ -936,6 +937,7 @@ ssd_status ssd_scan_ragged(const ssd_ragged_shape *shape, const ssd_packed *seq,
     char *ws = static_cast<char *>(workspace);
     a.ws_state = reinterpret_cast<float *>(ws + plan.state);
     a.ws_decay = reinterpret_cast<float *>(ws + plan.decay);
+    a.tables = reinterpret_cast<float *>(ws + plan.tables);
     a.status = static_cast<int *>(workspace);
     a.wait_cycles = wait_cycles_now();
     const bool bf16 = shape->io == SSD_BF16;

@@ -232,11 +232,11 @@ def test_scan_ragged_pieces_equal_the_whole(ssd):
         _check(s[0], last[0], tol * lastm[0])
 
 
-# The tensor-core form (bf16, headdim 64, d_state 128, pairs of heads).  One token's y sums, over the
-# tokens before it, C.B scores: P is rounded to bf16 (2^-8) after an exponential of a difference of two
-# sums (their size times u twice: cs below), S is rounded to bf16 where it meets C (2^-8), and y is
-# rounded (2^-8).  With Y the recurrence over absolute values: |dy| <= 2^-8 |y| + (1 + 2^-8) (2^-8 + 2^-12) Y,
-# 2^-12 being room for exponents (|cs| up to 500: 500 u ln 2 times a few) and float32 sums.
+# The tensor-core form (bf16, headdim 64, d_state 128, pairs of heads).  Within a chunk, a term of y is a
+# score rounded to bf16 (2^-8) times a w x rounded to bf16 (2^-8), or in the long form a P rounded once;
+# S is rounded to bf16 where it meets C (2^-8); y is rounded (2^-8).  With Y the recurrence over
+# absolute values: |dy| <= 2^-8 |y| + (1 + 2^-8) (2 2^-8 + 2^-16 + 2^-12) Y, 2^-12 being room for exponents (|cs|
+# up to 500: 500 u ln 2 times a few) and float32 sums.
 # The state: w x in two bf16 terms is within 2^-17 (a half step of 2^-9 of a rest of at most 2^-8), B exact;
 # w is within (|cs| + 8) 2 u, sums and decays of n / 128 chunks some 3 u each: (2^-17 + 2^-14) S.
 TC = [
@@ -246,7 +246,7 @@ TC = [
 
 
 def _tc_y(n, N, y, ym):
-    return 2.0 ** -8 * y.abs() + (1 + 2.0 ** -8) * (2.0 ** -8 + 2.0 ** -12) * ym + 1e-37
+    return 2.0 ** -8 * y.abs() + (1 + 2.0 ** -8) * (2.0 ** -7 + 2.0 ** -16 + 2.0 ** -12) * ym + 1e-37
 
 
 def _tc_s(n, s, sm):
