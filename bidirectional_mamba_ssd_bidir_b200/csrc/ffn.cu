@@ -427,6 +427,198 @@ __global__ void __launch_bounds__(kFThreads, 1) k_ffn(const __grid_constant__ Ff
     }
 }
 
+// ------------------------------------------------------------------ few tokens
+
+// With few tokens (decoding) the weights are all there is to read, and the tile above would leave its
+// rows empty and most SMs without a tile.  So the roles are exchanged: 128 rows of the weights are M,
+// the tokens N (16 to 256, more in groups of 256), D^T[128][tokens] = W u^T.  EPI_GLU: 64 rows of the
+// gate and the 64 rows beside them of the up projection make the 128.  Where the tiles are fewer than
+// the SMs, a cluster of `split` CTAs shares one: each takes a part of K, leaves its float32 sums in its
+// shared memory, and each adds up (in the order of the ranks, so the result does not depend on timing)
+// and finishes its share of the tokens from all of them.  The second product's weights do not depend
+// on the first: it is launched with programmatic dependent launch and has its first stages of them on
+// the way before it waits for h.
+//
+// Both forms measured at d_model 2048, d_ff 8192 (us, this one / the other): 3 tokens 26 / 99, 128: 40 /
+// 99, 256: 59 / 88, 512: 69 / 101, 1024: 120 / 126; at 768, 2048: 800 tokens 27 / 36.  Past 1024 tokens the
+// persistent tiles fill the SMs and hide their epilogues.
+constexpr int kFewMax = 1024;
+template <int N> struct FewTile {
+    static constexpr uint32_t kW = 128 * 128, kU = N * 128, kStage = kW + kU;
+    // two CTAs to an SM, or one of 256 tokens
+    static constexpr int kRoom = N == 256 ? 4 * kStage : 110592, kStages = kRoom / kStage > 6 ? 6 : kRoom / kStage;
+    static constexpr uint32_t kBar = kStages * kStage;          // the sums [N][128] lie over the stages
+    static constexpr uint32_t kMisc = (kBar + (2 * kStages + 1) * 8 + 15) & ~15u;
+    static constexpr uint32_t kSmem = kMisc + 32 + 1024;
+    static_assert(N * 128 * 4 <= kBar, "");
+    static_assert((N == 256 ? 1 : 2) * (kSmem + 1024) <= 233472, "");
+};
+struct FewParams {
+    CUtensorMap w, u;
+    int rows, K, T, up_row;        // rows of the output (d_ff or d_model); tokens
+    int split, save, gelu, wait_prior;
+    __nv_bfloat16 *out, *gu;       // out [T][rows]; gu [T][2 rows]
+    int *status;
+    long long wait_cycles;
+};
+
+template <int EPI, int N>
+__global__ void __launch_bounds__(kFThreads) k_ffn_few(const __grid_constant__ FewParams prm) {
+    using L = FewTile<N>;
+    constexpr int S = L::kStages, kTmemCols = N < 32 ? 32 : N;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(sm);
+    auto bar = [&](int i) { return sbase + L::kBar + 8u * i; };   // full 0 .., empty S .., 2 S: all products done
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + L::kMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + L::kMisc + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % prm.split, tile = blockIdx.x / prm.split, tok0 = N * blockIdx.y, ntok = min(N, prm.T - tok0);
+    const int nk = (prm.K + kFK - 1) / kFK, k0 = nk * rank / prm.split, k1 = nk * (rank + 1) / prm.split;
+    constexpr int kRows = EPI == EPI_GLU ? 64 : 128;              // output rows of a tile
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        *reinterpret_cast<volatile long long *>(abort_flag + 1) = prm.wait_cycles;
+        for (int i = 0; i < 2 * S + 1; ++i) mbar_init(bar(i), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "n"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (warp == 0) {
+        if (lane == 0) {
+            auto weights = [&](int kt, int st) {
+                const uint32_t at = sbase + st * L::kStage;
+                mbar_expect_tx(bar(st), L::kStage);
+                if (EPI == EPI_GLU) {
+                    tma_load_2d(at, &prm.w, kt * kFK, kRows * tile, bar(st));
+                    tma_load_2d(at + L::kW / 2, &prm.w, kt * kFK, prm.up_row + kRows * tile, bar(st));
+                } else {
+                    tma_load_2d(at, &prm.w, kt * kFK, kRows * tile, bar(st));
+                }
+            };
+            auto tokens = [&](int kt, int st) { tma_load_2d(sbase + st * L::kStage + L::kW, &prm.u, kt * kFK, tok0, bar(st)); };
+            const int head = min(S, k1 - k0);
+            for (int i = 0; i < head; ++i) weights(k0 + i, i);
+            if (prm.wait_prior) {
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                asm volatile("fence.proxy.async;" ::: "memory");
+            }
+            for (int i = 0; i < head; ++i) tokens(k0 + i, i);
+            int i = head;
+            for (; i < k1 - k0; ++i) {
+                const int st = i % S;
+                if (!mbar_wait(bar(S + st), (uint32_t)(i / S - 1) & 1, 1u, abort_flag, prm.status, 181)) break;
+                weights(k0 + i, st);
+                tokens(k0 + i, st);
+            }
+            if (*abort_flag)
+                for (int x = i - 1; x >= 0 && x >= i - S; --x) mbar_drain(bar(x % S), (uint32_t)(x / S) & 1, prm.wait_cycles);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const uint32_t id = idesc(N, 0, 0);
+        for (int i = 0; i < k1 - k0; ++i) {
+            const int st = i % S;
+            if (!mbar_wait(bar(st), (uint32_t)(i / S) & 1, 0xffffffffu, abort_flag, prm.status, 182)) break;
+            tc_fence_after();
+            const uint32_t at = sbase + st * L::kStage;
+            const SDesc dw = make_sdesc(at, 16, 1024), du = make_sdesc(at + L::kW, 16, 1024);
+#pragma unroll
+            for (int ks = 0; ks < kFK / 16; ++ks) mma_ss_w(tmem, dw.at(ks * 32), du.at(ks * 32), id, (i | ks) != 0);
+            mma_commit_w(bar(S + st));
+        }
+        mma_commit_w(bar(2 * S));
+        __syncwarp();
+    }
+    // every product of this CTA is done (and with them the reads of the stages)
+    const bool done = mbar_wait(bar(2 * S), 0, 0xffffffffu, abort_flag, prm.status, 183);
+    __syncthreads();
+    if (warp >= 2 && done) {
+        tc_fence_after();
+        const int qd = warp & 3;
+        float *sum = reinterpret_cast<float *>(sm) + 32 * qd + lane;
+        const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16);
+#pragma unroll
+        for (int c = 0; c < N; c += 16) {
+            float v[16];
+            tmem_ld16(tl + c, v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) sum[(c + e) * 128] = k1 > k0 ? v[e] : 0.f;   // a part without a k step adds nothing
+        }
+        tc_fence_before();
+    }
+    if (prm.split > 1) cluster_sync_all();
+    else __syncthreads();
+    if (!*abort_flag) {
+        // tokens rank, rank + split, ..: 16 or 32 threads to one, four rows of the weights each (the row
+        // counts are multiples of 8)
+        constexpr int kPer = kRows / 4, kGroups = kFThreads / kPer;
+        const int f = 4 * (threadIdx.x % kPer), grp = threadIdx.x / kPer, row = kRows * tile + f, step = prm.split * kGroups;
+        if (row < prm.rows) {
+            // the parts' sums of column c and weight rows l ..: all on the way at once, added in order
+            auto total = [&](int c, int l, float (&t)[4]) {
+                if (prm.split == 1) {
+                    const float4 v = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm) + c * 128 + l);
+                    t[0] = v.x; t[1] = v.y; t[2] = v.z; t[3] = v.w;
+                    return;
+                }
+                const uint32_t at = sbase + 4u * (c * 128 + l);
+                float4 v[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    v[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (r < prm.split)
+                        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                     : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w) : "r"(in_cta(at, r)));
+                }
+                t[0] = t[1] = t[2] = t[3] = 0.f;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    t[0] += v[r].x; t[1] += v[r].y; t[2] += v[r].z; t[3] += v[r].w;
+                }
+            };
+            auto store = [&](__nv_bfloat16 *to, const float (&t)[4]) {
+                *reinterpret_cast<uint2 *>(to) = make_uint2(pack_bf16(t[0], t[1]), pack_bf16(t[2], t[3]));
+            };
+            for (int c = rank + prm.split * grp; c < ntok; c += step) {
+                const long long t = tok0 + c;
+                if (EPI == EPI_GLU) {
+                    float g[4], p[4], act[4], der[4];
+                    total(c, f, g);
+                    total(c, 64 + f, p);
+                    activation(g, prm.gelu, act, der);
+                    if (prm.save) {
+                        store(prm.gu + t * 2 * prm.rows + row, g);
+                        store(prm.gu + t * 2 * prm.rows + prm.rows + row, p);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) p[e] *= act[e];
+                    store(prm.out + t * prm.rows + row, p);
+                } else {
+                    float d[4];
+                    total(c, f, d);
+                    store(prm.out + t * prm.rows + row, d);
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    // the others' sums are read until all are through
+    if (prm.split > 1) cluster_sync_all();
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
+    }
+}
+
 // ------------------------------------------------------------------ host side
 
 // [rows][cols] bf16, rows `ld` elements apart; box [box_rows][64], 128-byte swizzle
@@ -492,11 +684,66 @@ FfnProb product(int M, int N, int K, bool a_mn, bool b_mn) {
     return q;
 }
 
+template <int EPI, int N> cudaError_t run_few(FewParams &prm, cudaStream_t st) {
+    using L = FewTile<N>;
+    const int tiles = (prm.rows + (EPI == EPI_GLU ? 63 : 127)) / (EPI == EPI_GLU ? 64 : 128), nk = (prm.K + kFK - 1) / kFK,
+              groups = (prm.T + N - 1) / N;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    // as many parts of K as leave each CTA four steps and the tiles one wave
+    prm.split = 1;
+    while (prm.split < 8 && 2 * prm.split * tiles * groups <= sms && nk / (2 * prm.split) >= 4) prm.split *= 2;
+    auto *kernel = k_ffn_few<EPI, N>;
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kSmem)) != cudaSuccess) return e;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = prm.split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(tiles * prm.split, groups);
+    cfg.blockDim = dim3(kFThreads);
+    cfg.dynamicSmemBytes = L::kSmem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = prm.wait_prior ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, prm);
+}
+
+template <int EPI> cudaError_t run_few_any(FewParams &prm, const void *w, int w_rows, const void *u, cudaStream_t st) {
+    const int n = prm.T <= 16 ? 16 : prm.T <= 32 ? 32 : prm.T <= 64 ? 64 : prm.T <= 128 ? 128 : 256;
+    if (!map_of(&prm.w, w, w_rows, prm.K, prm.K, EPI == EPI_GLU ? 64 : 128) || !map_of(&prm.u, u, prm.T, prm.K, prm.K, n))
+        return cudaErrorInvalidValue;
+    switch (n) {
+        case 16: return run_few<EPI, 16>(prm, st);
+        case 32: return run_few<EPI, 32>(prm, st);
+        case 64: return run_few<EPI, 64>(prm, st);
+        case 128: return run_few<EPI, 128>(prm, st);
+        default: return run_few<EPI, 256>(prm, st);
+    }
+}
+
+cudaError_t launch_ffn_few(const FfnArgs &a, cudaStream_t st) {
+    FewParams prm;
+    memset(&prm, 0, sizeof prm);
+    prm.rows = a.F; prm.K = a.D; prm.T = a.T; prm.up_row = a.F; prm.gelu = a.gelu; prm.save = a.gu != nullptr;
+    prm.out = static_cast<__nv_bfloat16 *>(a.h); prm.gu = static_cast<__nv_bfloat16 *>(a.gu);
+    prm.status = a.status; prm.wait_cycles = a.wait_cycles;
+    cudaError_t e = run_few_any<EPI_GLU>(prm, a.W_in, 2 * a.F, a.u, st);
+    if (e != cudaSuccess) return e;
+    prm.rows = a.D; prm.K = a.F; prm.save = 0; prm.wait_prior = 1;
+    prm.out = static_cast<__nv_bfloat16 *>(a.out);
+    return run_few_any<EPI_PLAIN>(prm, a.W_out, a.D, a.h, st);
+}
+
 }  // namespace
 
 bool ffn_supported() { return get_encode() != nullptr; }
 
 cudaError_t launch_ffn(const FfnArgs &a, cudaStream_t st) {
+    if (a.T <= kFewMax) return launch_ffn_few(a, st);
     FfnParams prm;
     memset(&prm, 0, sizeof prm);
     prm.nprob = 1; prm.gelu = a.gelu; prm.status = a.status; prm.wait_cycles = a.wait_cycles;
