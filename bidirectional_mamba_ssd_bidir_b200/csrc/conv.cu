@@ -42,6 +42,23 @@ struct Walk {
             hi = q.tokens;
         }
     }
+    // The same for a whole warp: one look at 32 starts at a time (the search above is a chain of loads,
+    // and a run's first rows wait for it).
+    __device__ __forceinline__ void find_warp(const Packed &q, int t) {
+        if (!q.cu) {
+            find(q, t);
+            return;
+        }
+        const int lane = threadIdx.x & 31;
+        int i = -1;
+        for (int b = 0; b < q.nseq; b += 32) {
+            const int n = __popc(__ballot_sync(0xffffffffu, b + lane < q.nseq && seq_start(q, b + lane) <= t));
+            i += n;
+            if (n < 32) break;
+        }
+        set(q, i);
+        if (s >= 0 && t >= hi) set(q, q.nseq);
+    }
     // the sequence of row t; rows in none get an index outside [0, nseq)
     __device__ __forceinline__ void find(const Packed &q, int t) {
         set(q, seq_find(q, t));
@@ -138,20 +155,27 @@ __global__ void __launch_bounds__(kThreads) k_conv(const __grid_constant__ ConvA
         conv_state<T, V, KT>(a, unit - a.units, c0);
         return;
     }
-    if (c0 >= a.C) return;
+    const bool live = c0 < a.C;                      // (a whole warp is needed to find the sequence)
     const int u0 = unit * a.run, n = min(a.run, a.seq.tokens - u0);
     const int first = a.dir > 0 ? u0 : u0 + n - 1;
     const T *xc = static_cast<const T *>(a.x) + (long long)first * a.ldx + c0;
     T *yc = static_cast<T *>(a.y) + (long long)first * a.ldy + c0;
     const long long sx = a.dir * a.ldx, sy = a.dir * a.ldy;
-    R next[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
-        if (i < n) next[i] = *reinterpret_cast<const R *>(xc + i * sx);
-    Walk w;
-    w.find(a.seq, first);
+    // everything the first rows need is asked for at once: rows, the rows before them, taps, offsets
+    R next[kRows], back[KM > 1 ? KM - 1 : 1];
     float wr[KM][V], b[V], win[KM][V];
-    load_taps<T, V, KM>(a, K, c0, wr, b);
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+            if (i < n) next[i] = *reinterpret_cast<const R *>(xc + i * sx);
+        const int behind = a.dir > 0 ? first : a.seq.tokens - 1 - first;
+#pragma unroll
+        for (int j = 0; j < KM - 1; ++j) back[j] = *reinterpret_cast<const R *>(xc - min(j + 1, behind) * sx);
+        load_taps<T, V, KM>(a, K, c0, wr, b);
+    }
+    Walk w;
+    w.find_warp(a.seq, first);
+    if (!live) return;
     // k: the present row's place in its sequence, in scan order; left: rows of the sequence from it on
     int k = a.dir > 0 ? first - w.lo : w.hi - 1 - first, left = a.dir > 0 ? w.hi - first : first - w.lo + 1;
 #pragma unroll
@@ -159,9 +183,31 @@ __global__ void __launch_bounds__(kThreads) k_conv(const __grid_constant__ ConvA
 #pragma unroll
         for (int v = 0; v < V; ++v) win[j][v] = 0.f;
         // before its first shift the window holds the row j + 1 steps back
-        if (j < K - 1 && k > j) unpack<T, V>(*reinterpret_cast<const R *>(xc - (j + 1) * sx), win[j]);
+        if (j < KM - 1 && j < K - 1 && k > j) unpack<T, V>(back[j < KM - 1 ? j : 0], win[j]);
     }
     const int skip = a.slots.pool_in ? K - 1 : 0;   // those outputs belong to the per-sequence CTAs
+    // the next row into the window, and its output
+    auto step = [&](const R &in, R &out) {
+#pragma unroll
+        for (int j = KM - 1; j > 0; --j)
+#pragma unroll
+            for (int v = 0; v < V; ++v) win[j][v] = win[j - 1][v];
+        unpack<T, V>(in, win[0]);
+        float acc[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = b[v];
+#pragma unroll
+        for (int j = KM - 1; j >= 0; --j) {
+            if (KT == 0 && j >= K) continue;
+            fma_v<V>(wr[j], win[j], acc);
+        }
+        if (a.silu) {
+            float sg[V];
+            sigmoids<V>(acc, sg);
+            mul_v<V>(acc, sg, acc);
+        }
+        out = pack<T, V>(acc);
+    };
     for (int i0 = 0; i0 < n; i0 += kRows) {
         R cur[kRows];
 #pragma unroll
@@ -169,6 +215,18 @@ __global__ void __launch_bounds__(kThreads) k_conv(const __grid_constant__ ConvA
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
             if (i0 + kRows + i < n) next[i] = *reinterpret_cast<const R *>(xc + (i0 + kRows + i) * sx);
+        // eight rows of one sequence, none of them the per-sequence CTAs' (the same for all threads)
+        if (i0 + kRows <= n && left >= kRows && k >= skip && w.s >= 0 && w.s < a.seq.nseq) {
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                R out;
+                step(cur[i], out);
+                *reinterpret_cast<R *>(yc + (i0 + i) * sy) = out;
+            }
+            k += kRows;
+            left -= kRows;
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             if (i0 + i >= n) break;
@@ -181,28 +239,9 @@ __global__ void __launch_bounds__(kThreads) k_conv(const __grid_constant__ ConvA
 #pragma unroll
                     for (int v = 0; v < V; ++v) win[j][v] = 0.f;
             }
-#pragma unroll
-            for (int j = KM - 1; j > 0; --j)
-#pragma unroll
-                for (int v = 0; v < V; ++v) win[j][v] = win[j - 1][v];
-            unpack<T, V>(cur[i], win[0]);
-            float acc[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] = b[v];
-#pragma unroll
-            for (int j = KM - 1; j >= 0; --j) {
-                if (KT == 0 && j >= K) continue;
-#pragma unroll
-                for (int v = 0; v < V; ++v) acc[v] = fmaf(wr[j][v], win[j][v], acc[v]);
-            }
-            if (a.silu) {
-                float sg[V];
-                sigmoids<V>(acc, sg);
-#pragma unroll
-                for (int v = 0; v < V; ++v) acc[v] *= sg[v];
-            }
-            if (k >= skip && w.s >= 0 && w.s < a.seq.nseq)
-                *reinterpret_cast<R *>(yc + (i0 + i) * sy) = pack<T, V>(acc);
+            R out;
+            step(cur[i], out);
+            if (k >= skip && w.s >= 0 && w.s < a.seq.nseq) *reinterpret_cast<R *>(yc + (i0 + i) * sy) = out;
             ++k;
             --left;
         }
@@ -223,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
     const int K = KT > 0 ? KT : a.K;
     const int unit = blockIdx.x / a.cblocks, c0 = ((blockIdx.x % a.cblocks) * kThreads + threadIdx.x) * V;
     if (blockIdx.x == 0) check_offsets(a.seq, a.status);
-    if (c0 >= a.C) return;
+    const bool live = c0 < a.C;
     const int u0 = unit * a.run, n = min(a.run, a.seq.tokens - u0);
     const int first = a.dir > 0 ? u0 : u0 + n - 1;
     const int room = a.dir > 0 ? a.seq.tokens - first : first + 1;   // rows from `first` on, in scan order
@@ -233,23 +272,29 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
     T *yc = static_cast<T *>(a.y) + (long long)first * a.ldy + c0;
     const long long sx = a.dir * a.ldx, sg_ = a.dir * a.ldg, sy = a.dir * a.ldy;
     constexpr int U = 4;
-    R nx[U], ng[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-        if (i < steps) {
-            nx[i] = *reinterpret_cast<const R *>(xc + i * sx);
-            ng[i] = *reinterpret_cast<const R *>(gc + i * sg_);
-        }
-    Walk w;
-    w.find(a.seq, first);
+    R nx[U], ng[U], back[KM > 1 ? KM - 1 : 1];
     float wr[KM][V], b[V], win[KM][V], gs[KM][V], gw[KM][V], gb[V];
-    load_taps<T, V, KM>(a, K, c0, wr, b);
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (i < steps) {
+                nx[i] = *reinterpret_cast<const R *>(xc + i * sx);
+                ng[i] = *reinterpret_cast<const R *>(gc + i * sg_);
+            }
+        const int behind = a.dir > 0 ? first : a.seq.tokens - 1 - first;
+#pragma unroll
+        for (int j = 0; j < KM - 1; ++j) back[j] = *reinterpret_cast<const R *>(xc - min(j + 1, behind) * sx);
+        load_taps<T, V, KM>(a, K, c0, wr, b);
+    }
+    Walk w;
+    w.find_warp(a.seq, first);
+    if (!live) return;
     int k = a.dir > 0 ? first - w.lo : w.hi - 1 - first, left = a.dir > 0 ? w.hi - first : first - w.lo + 1;
 #pragma unroll
     for (int j = 0; j < KM; ++j) {
 #pragma unroll
         for (int v = 0; v < V; ++v) win[j][v] = gs[j][v] = gw[j][v] = 0.f;
-        if (j < K - 1 && k > j) unpack<T, V>(*reinterpret_cast<const R *>(xc - (j + 1) * sx), win[j]);
+        if (j < KM - 1 && j < K - 1 && k > j) unpack<T, V>(back[j < KM - 1 ? j : 0], win[j]);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) gb[v] = 0.f;
@@ -258,6 +303,45 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
 #pragma unroll
     for (int j = 0; j < KM; ++j) place[j] = -1;
     bool inseq = w.s >= 0 && w.s < a.seq.nseq;
+    // gs of the row in win[0]
+    auto grad = [&](const R &gin, float (&g)[V]) {
+        unpack<T, V>(gin, g);
+        if (a.silu) {
+            float s[V], sg[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] = b[v];
+#pragma unroll
+            for (int j = KM - 1; j >= 0; --j) {
+                if (KT == 0 && j >= K) continue;
+                fma_v<V>(wr[j], win[j], s);
+            }
+            sigmoids<V>(s, sg);
+            // sg (1 + s (1 - sg)) = sg + t (1 - sg), t = s sg
+            float t[V], d[V];
+            mul_v<V>(s, sg, t);
+#pragma unroll
+            for (int v = 0; v < V; ++v) d[v] = 1.f - sg[v];
+            fma_v<V>(t, d, sg, d);
+            mul_v<V>(g, d, g);
+        }
+    };
+    auto shift = [&]() {
+#pragma unroll
+        for (int j = KM - 1; j > 0; --j)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                win[j][v] = win[j - 1][v];
+                gs[j][v] = gs[j - 1][v];
+            }
+    };
+    auto sums = [&]() {                              // gw and gb of the row in win[0], gs[0]
+        add_v<V>(gb, gs[0], gb);
+#pragma unroll
+        for (int j = 0; j < KM; ++j) {
+            if (KT == 0 && j >= K) continue;
+            fma_v<V>(gs[0], win[j], gw[j]);
+        }
+    };
     for (int i0 = 0; i0 < n + K - 1; i0 += U) {
         R cx[U], cg[U];
 #pragma unroll
@@ -271,19 +355,35 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
                 nx[i] = *reinterpret_cast<const R *>(xc + (i0 + U + i) * sx);
                 ng[i] = *reinterpret_cast<const R *>(gc + (i0 + U + i) * sg_);
             }
+        // rows of one sequence, K - 1 rows into it and into the run (the same for all threads)
+        if (KT > 0 && i0 >= K - 1 && i0 + U <= n && left >= U && k >= K - 1 && inseq) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                shift();
+                unpack<T, V>(cx[i], win[0]);
+                grad(cg[i], gs[0]);
+                sums();
+                float gx[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) gx[v] = 0.f;
+                // entry j of gs is K - 1 - j rows ahead of the row K - 1 back
+#pragma unroll
+                for (int j = 0; j < KM; ++j) fma_v<V>(wr[KM - 1 - j], gs[j], gx);
+                *reinterpret_cast<R *>(yc + (i0 + i - (K - 1)) * sy) = pack<T, V>(gx);
+            }
+            k += U;
+            left -= U;
+#pragma unroll
+            for (int j = 0; j < KM; ++j) place[j] = k - 1 - j;
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int tau = i0 + i;
             if (tau >= n + K - 1) break;
+            shift();
 #pragma unroll
-            for (int j = KM - 1; j > 0; --j) {
-                place[j] = place[j - 1];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    win[j][v] = win[j - 1][v];
-                    gs[j][v] = gs[j - 1][v];
-                }
-            }
+            for (int j = KM - 1; j > 0; --j) place[j] = place[j - 1];
             if (tau < steps) {
                 if (left == 0) {
                     w.find(a.seq, first + a.dir * tau);
@@ -296,33 +396,12 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
                         for (int v = 0; v < V; ++v) win[j][v] = 0.f;
                 }
                 unpack<T, V>(cx[i], win[0]);
-                float g[V];
-                unpack<T, V>(cg[i], g);
-                if (a.silu) {
-                    float s[V], sg[V];
-#pragma unroll
-                    for (int v = 0; v < V; ++v) s[v] = b[v];
-#pragma unroll
-                    for (int j = KM - 1; j >= 0; --j) {
-                        if (KT == 0 && j >= K) continue;
-#pragma unroll
-                        for (int v = 0; v < V; ++v) s[v] = fmaf(wr[j][v], win[j][v], s[v]);
-                    }
-                    sigmoids<V>(s, sg);
-#pragma unroll
-                    for (int v = 0; v < V; ++v) g[v] *= sg[v] * fmaf(s[v], 1.f - sg[v], 1.f);
-                }
+                grad(cg[i], gs[0]);
                 place[0] = inseq ? k : -1;
-                const bool sum = inseq && tau < n;
+                if (!inseq)
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    gs[0][v] = inseq ? g[v] : 0.f;
-                    if (sum) {
-                        gb[v] += g[v];
-#pragma unroll
-                        for (int j = 0; j < KM; ++j) gw[j][v] = fmaf(g[v], win[j][v], gw[j][v]);
-                    }
-                }
+                    for (int v = 0; v < V; ++v) gs[0][v] = 0.f;
+                if (inseq && tau < n) sums();
                 ++k;
                 --left;
             } else {
@@ -342,17 +421,10 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
                     if (j == K - 1) p0 = place[j];
 #pragma unroll
                 for (int j = 0; j < KM; ++j) {
-                    if (j >= K) continue;
-                    // (K - 1 - j) steps ahead of that row: tap wr[K - 1 - j]
-                    const bool same = place[j] == p0 + (K - 1 - j);
-                    if (same) {
+                    if (j >= K || place[j] != p0 + (K - 1 - j)) continue;
 #pragma unroll
-                        for (int q = 0; q < KM; ++q)
-                            if (q == K - 1 - j) {
-#pragma unroll
-                                for (int v = 0; v < V; ++v) gx[v] = fmaf(wr[q][v], gs[j][v], gx[v]);
-                            }
-                    }
+                    for (int q = 0; q < KM; ++q)
+                        if (q == K - 1 - j) fma_v<V>(wr[q], gs[j], gx);
                 }
                 // a row in no sequence has gradient zero
                 if (p0 < 0)
@@ -372,19 +444,24 @@ __global__ void __launch_bounds__(kThreads) k_conv_bwd(const __grid_constant__ C
     }
 }
 
-// Adds the runs' partial sums: one thread per (tap or bias, channel), the runs in four interleaved
-// sums that a fixed tree joins.
-__global__ void __launch_bounds__(kThreads) k_conv_sum(const __grid_constant__ ConvArgs a) {
-    const int K = a.K;
-    const long long i = (long long)blockIdx.x * kThreads + threadIdx.x, cols = (long long)(K + 1) * a.C;
-    if (i >= cols) return;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    int u = 0;
-    for (; u + 4 <= a.units; u += 4)
+// Adds the runs' partial sums: 32 columns (tap or bias, channel) a CTA, every eighth run a warp, the
+// warps' sums joined in their order.
+constexpr int kSumThreads = 256;
+__global__ void __launch_bounds__(kSumThreads) k_conv_sum(const __grid_constant__ ConvArgs a) {
+    __shared__ float part[kSumThreads / 32][32];
+    const int K = a.K, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long i = (long long)blockIdx.x * 32 + lane, cols = (long long)(K + 1) * a.C;
+    float s = 0.f;
+    if (i < cols) {
+#pragma unroll 4
+        for (int u = warp; u < a.units; u += kSumThreads / 32) s += a.part[u * cols + i];
+    }
+    part[warp][lane] = s;
+    __syncthreads();
+    if (warp > 0 || i >= cols) return;
+    float t = 0.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s[q] += a.part[(u + q) * cols + i];
-    for (; u < a.units; ++u) s[0] += a.part[u * cols + i];
-    const float t = (s[0] + s[1]) + (s[2] + s[3]);
+    for (int w = 0; w < kSumThreads / 32; ++w) t += part[w][lane];
     const int k = (int)(i / a.C), c = (int)(i % a.C);
     if (k < K) a.gw[(long long)c * K + k] = t;
     else if (a.gb) a.gb[c] = t;
@@ -442,7 +519,7 @@ cudaError_t launch_conv_bwd(ConvArgs a, bool bf16, cudaStream_t st) {
     cudaError_t e = bf16 ? run_conv<__nv_bfloat16, true>(a, vec_ok(a, 2), st) : run_conv<float, true>(a, vec_ok(a, 4), st);
     if (e != cudaSuccess) return e;
     const long long cols = (long long)(a.K + 1) * a.C;
-    k_conv_sum<<<(unsigned)((cols + kThreads - 1) / kThreads), kThreads, 0, st>>>(a);
+    k_conv_sum<<<(unsigned)((cols + 31) / 32), kSumThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 

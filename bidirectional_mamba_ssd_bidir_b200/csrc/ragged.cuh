@@ -191,6 +191,8 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
 template <typename T, int V> struct Vec;
 template <> struct Vec<__nv_bfloat16, 4> { using type = uint2; };
 template <> struct Vec<float, 4> { using type = uint4; };
+template <> struct Vec<__nv_bfloat16, 2> { using type = uint32_t; };
+template <> struct Vec<float, 2> { using type = uint2; };
 template <> struct Vec<__nv_bfloat16, 1> { using type = __nv_bfloat16; };
 template <> struct Vec<float, 1> { using type = float; };
 
@@ -224,27 +226,63 @@ __device__ __forceinline__ float rcpa(float x) {
     return y;
 }
 
-// sigma[i] = 1 / (1 + e^-v[i]).  With e = e^-|v| <= 1 it is 1 / (1 + e) or e / (1 + e), which keeps
-// its relative accuracy on both sides and stays finite; the V divisions share one reciprocal, of the
-// product of the denominators (each within [1, 2], at most 16).  The denominator of a NaN counts as
-// 2, so it spoils its own channel alone.
-template <int V> __device__ __forceinline__ void sigmoids(const float (&v)[V], float (&sg)[V]) {
-    float e[V], d[V];
+// Pairs of float32 in one instruction (the packed forms of sm_100): a b + c, a b, a + b.
+__device__ __forceinline__ void fma2_to(float &d0, float &d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+template <int V> __device__ __forceinline__ void fma_v(const float (&a)[V], const float (&b)[V], const float (&c)[V], float (&d)[V]) {
+    if constexpr (V % 2 == 0) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        e[i] = ex2a(-1.4426950408889634f * fabsf(v[i]));
-        d[i] = 1.f + fminf(e[i], 1.f);
-    }
-    if constexpr (V == 4) {
-        const float p01 = d[0] * d[1], p23 = d[2] * d[3], r = rcpa(p01 * p23);
-        const float r01 = r * p23, r23 = r * p01;
-        const float inv[4] = {r01 * d[1], r01 * d[0], r23 * d[3], r23 * d[2]};
-#pragma unroll
-        for (int i = 0; i < V; ++i) sg[i] = (v[i] >= 0.f ? 1.f : e[i]) * inv[i];
+        for (int i = 0; i < V; i += 2) fma2_to(d[i], d[i + 1], a[i], a[i + 1], b[i], b[i + 1], c[i], c[i + 1]);
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) sg[i] = (v[i] >= 0.f ? 1.f : e[i]) * rcpa(d[i]);
+        for (int i = 0; i < V; ++i) d[i] = fmaf(a[i], b[i], c[i]);
     }
+}
+// d += a b
+template <int V> __device__ __forceinline__ void fma_v(const float (&a)[V], const float (&b)[V], float (&d)[V]) { fma_v<V>(a, b, d, d); }
+template <int V> __device__ __forceinline__ void mul_v(const float (&a)[V], const float (&b)[V], float (&d)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+            asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+                "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+                : "=f"(d[i]), "=f"(d[i + 1]) : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = a[i] * b[i];
+    }
+}
+template <int V> __device__ __forceinline__ void add_v(const float (&a)[V], const float (&b)[V], float (&d)[V]) {
+    if constexpr (V % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+            asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+                "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+                : "=f"(d[i]), "=f"(d[i + 1]) : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = a[i] + b[i];
+    }
+}
+
+// sigma[i] = 1 / (1 + e^-v[i]), each from one ex2 and one rcp (approximations within 2 ulp; results
+// below 2^-126 flush to zero).  e^-v past the float range makes it 0, as it should be.
+template <int V> __device__ __forceinline__ void sigmoids(const float (&v)[V], float (&sg)[V]) {
+    float c[V], e[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = -1.4426950408889634f;
+    mul_v<V>(v, c, e);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        e[i] = ex2a(e[i]);
+        c[i] = 1.f;
+    }
+    add_v<V>(e, c, e);
+#pragma unroll
+    for (int i = 0; i < V; ++i) sg[i] = rcpa(e[i]);
 }
 
 }  // namespace
