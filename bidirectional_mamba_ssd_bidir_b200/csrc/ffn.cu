@@ -18,8 +18,9 @@
 // k_ffn, one kernel for all products D[M][N] = A B: persistent, warp-specialised, tiles of
 // 128 CG x 256 over a group of CG CTAs (CG = 2: a CTA pair shares one tcgen05.mma of M = 256, each
 // CTA holding half of A's rows and half of B's columns).  Warp 0 feeds the stage ring by TMA, warp 1
-// of the group's first CTA issues the MMAs (N 256, K 16), warps 2-5 drain one 256-column TMEM
-// accumulator while the other fills, each warp storing its own 32 rows through its own staging boxes.
+// of the group's first CTA issues the MMAs (N 256, K 16), warps 2-5 (2-9 with the activation's
+// gradient) drain one 256-column TMEM accumulator while the other fills, each warp storing its own 32
+// rows through its own staging boxes.
 // An operand may lie along K (K-major: rows of 64 k, the descriptor's usual form) or across it
 // (MN-major: 64 x 64 boxes, 64 rows or columns wide), so nothing is transposed in memory.  Edges of
 // any size come out of the tensor maps: loads outside a matrix read zero, stores there are dropped.
@@ -43,13 +44,18 @@ constexpr int kFK = 64;                          // K of a stage
 constexpr uint32_t kFBox = 128 * 128;            // 128 rows of 64 bf16
 constexpr uint32_t kFOutBox = 32 * 128;          // one warp's 32 rows of 64 columns
 constexpr int kFThreads = 192, kFMaxProb = 3;
+// The activation's gradient takes more work an element than one warp per SM sub-partition does in the
+// time of a tile: eight epilogue warps there, each half of the columns.
+template <int EPI> constexpr int kEpiWarps = EPI == EPI_GLU_BWD ? 8 : 4;
+template <int EPI> constexpr int kFfnThreads = 64 + 32 * kEpiWarps<EPI>;
+constexpr uint32_t kNarrowBox = 32 * 64;         // one warp's 32 rows of 32 columns
 
 template <int EPI, int CG> struct FfnTile {
     static constexpr uint32_t kA = kFBox, kB = CG == 2 ? kFBox : 2 * kFBox, kStage = kA + kB;
     static constexpr int kBoxes = EPI == EPI_PLAIN ? 2 : 3;       // staging boxes of an epilogue warp
     static constexpr int kStages = CG == 2 ? (EPI == EPI_PLAIN ? 6 : 5) : (EPI == EPI_PLAIN ? 4 : 3);
     static constexpr uint32_t kOut = kStages * kStage;
-    static constexpr uint32_t kBar = kOut + 4 * kBoxes * kFOutBox;
+    static constexpr uint32_t kBar = kOut + (EPI == EPI_GLU_BWD ? 8 * 3 * kNarrowBox : 4 * kBoxes * kFOutBox);
     static constexpr int kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + 2, kDone = kAccEmpty + 2,
                          kBars = kDone + 1;
     static constexpr uint32_t kMisc = (kBar + kBars * 8 + 15) & ~15u;
@@ -99,21 +105,27 @@ template <int CG> __device__ __forceinline__ void pair_load(uint32_t dst, const 
             "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
             : "memory");
 }
+// One lane of a converged warp: a stage's four MMAs are issued inside one such branch (each electing its
+// own lane took 4 % longer over the whole block).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(e));
+    return e != 0;
+}
 template <int CG> __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-    if constexpr (CG == 1) mma_ss_w(d, a, b, id, acc);
+    if constexpr (CG == 1) mma_ss(d, a, b, id, acc);
     else
         asm volatile(
-            "{\n\t.reg .pred P, p;\n\telect.sync _|P, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-            "@P tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
             "l"(a), "l"(b), "r"(id), "r"(acc));
 }
 // arrives on the barrier at this offset of every CTA of the group once the MMAs issued so far are done
 template <int CG> __device__ __forceinline__ void pair_commit(uint32_t bar) {
-    if constexpr (CG == 1) mma_commit_w(bar);
+    if constexpr (CG == 1) mma_commit(bar);
     else
         asm volatile(
-            "{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\t"
-            "@P tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
             "h"((uint16_t)3)
             : "memory");
 }
@@ -157,7 +169,7 @@ __device__ __forceinline__ uint4 pack8(const float *v) {
 }
 
 template <int EPI, int CG>
-__global__ void __launch_bounds__(kFThreads, 1) k_ffn(const __grid_constant__ FfnParams prm) {
+__global__ void __launch_bounds__(kFfnThreads<EPI>, 1) k_ffn(const __grid_constant__ FfnParams prm) {
     using L = FfnTile<EPI, CG>;
     constexpr int S = L::kStages;
     constexpr int kTileN = EPI == EPI_GLU ? 128 : 256;   // output columns of a tile
@@ -175,7 +187,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_ffn(const __grid_constant__ Ff
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         *reinterpret_cast<volatile long long *>(abort_flag + 1) = prm.wait_cycles;
-        for (int i = 0; i < L::kBars; ++i) mbar_init(bar(i), (i == L::kAccEmpty || i == L::kAccEmpty + 1) ? 4u * CG : 1u);
+        for (int i = 0; i < L::kBars; ++i) mbar_init(bar(i), (i == L::kAccEmpty || i == L::kAccEmpty + 1) ? (uint32_t)(kEpiWarps<EPI> * CG) : 1u);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -262,15 +274,19 @@ __global__ void __launch_bounds__(kFThreads, 1) k_ffn(const __grid_constant__ Ff
                     tc_fence_after();
                     const uint32_t sa = sbase + st * L::kStage;
                     const SDesc da = make_sdesc(sa, la, 1024), db = make_sdesc(sa + L::kA, lb, 1024);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < kFK / 16; ++ks)
-                        pair_mma<CG>(tmem + 256u * acc, da.at(ks * ka), db.at(ks * kb), id, (kt | ks) != 0);
-                    pair_commit<CG>(bar(L::kEmpty + st));
+                        for (int ks = 0; ks < kFK / 16; ++ks)
+                            pair_mma<CG>(tmem + 256u * acc, da.at(ks * ka), db.at(ks * kb), id, (kt | ks) != 0);
+                        pair_commit<CG>(bar(L::kEmpty + st));
+                        if (kt == nk - 1) pair_commit<CG>(bar(L::kAccFull + acc));
+                    }
+                    __syncwarp();
                 }
                 if (!ok) break;
-                pair_commit<CG>(bar(L::kAccFull + acc));
             }
-            pair_commit<CG>(bar(L::kDone));
+            if (elect_one()) pair_commit<CG>(bar(L::kDone));
+            __syncwarp();
         }
         // both CTAs leave only after every MMA issued has completed
         if (lane == 0) mbar_drain(bar(L::kDone), 0, prm.wait_cycles);
@@ -293,6 +309,71 @@ __global__ void __launch_bounds__(kFThreads, 1) k_ffn(const __grid_constant__ Ff
             const FfnWhere w = tile_at<CG>(prm, t, kTileN);
             const FfnProb &q = prm.p[w.p];
             const int acc = tc & 1, m0 = w.m0 + 128 * rank + 32 * qd;
+            if constexpr (EPI == EPI_GLU_BWD) {
+                // this warp's 128 columns in four steps of 32; a step's g and p are loaded a step ahead,
+                // the first one's before the product is done
+                const int half = (warp - 2) >> 2, m = m0 + lane, c0 = 128 * half;
+                const __nv_bfloat16 *row = prm.gu + (long long)m * 2 * q.N + w.n0 + c0;
+                const uint32_t b = L::kOut + (uint32_t)(warp - 2) * 3 * kNarrowBox;
+                uint4 ng[4], np[4];
+                auto load = [&](int c) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        ng[i] = np[i] = make_uint4(0u, 0u, 0u, 0u);
+                        if (m < q.M && w.n0 + c0 + c + 8 * i < q.N) {   // N is a multiple of 8
+                            ng[i] = *reinterpret_cast<const uint4 *>(row + c + 8 * i);
+                            np[i] = *reinterpret_cast<const uint4 *>(row + q.N + c + 8 * i);
+                        }
+                    }
+                };
+                load(0);
+                if (!mbar_wait(bar(L::kAccFull + acc), (tc >> 1) & 1, MASK, abort_flag, prm.status, 144)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 128; c += 32) {
+                    float gh[32];
+                    tmem_ld32(tl + 256u * acc + c0 + c, gh);
+                    uint4 cg_[4], cp[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        cg_[i] = ng[i];
+                        cp[i] = np[i];
+                    }
+                    if (c + 32 < 128) load(c + 32);
+                    if (lane == 0) bulk_wait_read0();
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t ga[4] = {cg_[i].x, cg_[i].y, cg_[i].z, cg_[i].w}, pa[4] = {cp[i].x, cp[i].y, cp[i].z, cp[i].w};
+                        float gg[8], gp[8], hh[8];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float g4[4] = {bf16lo(ga[2 * e]), bf16hi(ga[2 * e]), bf16lo(ga[2 * e + 1]), bf16hi(ga[2 * e + 1])};
+                            const float p4[4] = {bf16lo(pa[2 * e]), bf16hi(pa[2 * e]), bf16lo(pa[2 * e + 1]), bf16hi(pa[2 * e + 1])};
+                            float act[4], der[4];
+                            activation(g4, prm.gelu, act, der);
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                const float d = gh[8 * i + 4 * e + z];
+                                gg[4 * e + z] = d * p4[z] * der[z];
+                                gp[4 * e + z] = d * act[z];
+                                hh[4 * e + z] = act[z] * p4[z];
+                            }
+                        }
+                        // rows of 64 bytes under the 64-byte swizzle
+                        const uint32_t at = b + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4);
+                        *reinterpret_cast<uint4 *>(sm + at) = pack8(gg);
+                        *reinterpret_cast<uint4 *>(sm + at + kNarrowBox) = pack8(gp);
+                        *reinterpret_cast<uint4 *>(sm + at + 2 * kNarrowBox) = pack8(hh);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (w.n0 + c0 + c < q.N)
+#pragma unroll
+                        for (int x = 0; x < 3; ++x) send(&q.d[x], b + x * kNarrowBox, w.n0 + c0 + c, m0);
+                    if (lane == 0) bulk_commit();
+                }
+            } else {
             if (!mbar_wait(bar(L::kAccFull + acc), (tc >> 1) & 1, MASK, abort_flag, prm.status, 144)) break;
             tc_fence_after();
             const uint32_t ta = tl + 256u * acc;
@@ -316,7 +397,7 @@ __global__ void __launch_bounds__(kFThreads, 1) k_ffn(const __grid_constant__ Ff
                     if (live) send(&q.d[0], b, w.n0 + c, m0);
                     if (lane == 0) bulk_commit();
                     ++used;
-                } else if (EPI == EPI_GLU) {
+                } else {
                     if (lane == 0) bulk_wait_read0();
                     __syncwarp();
                     const uint32_t b = boxes;
@@ -352,58 +433,8 @@ __global__ void __launch_bounds__(kFThreads, 1) k_ffn(const __grid_constant__ Ff
                         }
                     }
                     if (lane == 0) bulk_commit();
-                } else {
-                    const uint32_t b = boxes;
-                    const int m = m0 + lane;
-                    const __nv_bfloat16 *row = prm.gu + (long long)m * 2 * q.N + w.n0 + c;
-                    uint4 rg[8], ru[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        rg[i] = ru[i] = make_uint4(0u, 0u, 0u, 0u);
-                        if (m < q.M && w.n0 + c + 8 * i < q.N) {   // N is a multiple of 8
-                            rg[i] = *reinterpret_cast<const uint4 *>(row + 8 * i);
-                            ru[i] = *reinterpret_cast<const uint4 *>(row + q.N + 8 * i);
-                        }
-                    }
-                    if (lane == 0) bulk_wait_read0();
-                    __syncwarp();
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float gh[32];
-                        tmem_ld32(ta + c + 32 * x, gh);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4 a = rg[4 * x + i], u = ru[4 * x + i];
-                            const uint32_t ga[4] = {a.x, a.y, a.z, a.w}, ua[4] = {u.x, u.y, u.z, u.w};
-                            float gg[8], gp[8], hh[8];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float g4[4] = {bf16lo(ga[2 * e]), bf16hi(ga[2 * e]), bf16lo(ga[2 * e + 1]), bf16hi(ga[2 * e + 1])};
-                                const float u4[4] = {bf16lo(ua[2 * e]), bf16hi(ua[2 * e]), bf16lo(ua[2 * e + 1]), bf16hi(ua[2 * e + 1])};
-                                float act[4], der[4];
-                                activation(g4, prm.gelu, act, der);
-#pragma unroll
-                                for (int z = 0; z < 4; ++z) {
-                                    const float d = gh[8 * i + 4 * e + z];
-                                    gg[4 * e + z] = d * u4[z] * der[z];
-                                    gp[4 * e + z] = d * act[z];
-                                    hh[4 * e + z] = act[z] * u4[z];
-                                }
-                            }
-                            put(b, 4 * x + i, gg);
-                            put(b + kFOutBox, 4 * x + i, gp);
-                            put(b + 2 * kFOutBox, 4 * x + i, hh);
-                        }
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (live) {
-                        send(&q.d[0], b, w.n0 + c, m0);
-                        send(&q.d[1], b + kFOutBox, w.n0 + c, m0);
-                        send(&q.d[2], b + 2 * kFOutBox, w.n0 + c, m0);
-                    }
-                    if (lane == 0) bulk_commit();
                 }
+            }
             }
             // the accumulator has been read: the MMA warp may fill it again
             tc_fence_before();
@@ -621,14 +652,14 @@ __global__ void __launch_bounds__(kFThreads) k_ffn_few(const __grid_constant__ F
 
 // ------------------------------------------------------------------ host side
 
-// [rows][cols] bf16, rows `ld` elements apart; box [box_rows][64], 128-byte swizzle
-bool map_of(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+// [rows][cols] bf16, rows `ld` elements apart; box [box_rows][64 or 32], swizzled over its row of 128 or 64 bytes
+bool map_of(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows, uint32_t box_cols = 64) {
     EncodeTiled enc = get_encode();
     if (!enc) return false;
     const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * 2};
-    const cuuint32_t box[2] = {64, box_rows}, estr[2] = {1, 1};
+    const cuuint32_t box[2] = {box_cols, box_rows}, estr[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -662,7 +693,7 @@ template <int EPI, int CG> cudaError_t run_ffn(FfnParams &prm, cudaStream_t st) 
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(groups * CG);
-    cfg.blockDim = dim3(kFThreads);
+    cfg.blockDim = dim3(kFfnThreads<EPI>);
     cfg.dynamicSmemBytes = FfnTile<EPI, CG>::kSmem;
     cfg.stream = st;
     cfg.attrs = at;
@@ -775,8 +806,8 @@ cudaError_t launch_ffn_bwd(const FfnArgs &a, cudaStream_t st) {
     q = product(a.T, a.F, a.D, false, true);
     __nv_bfloat16 *ggu = static_cast<__nv_bfloat16 *>(a.ggu);
     if (!operand(&q.a, a.gy, a.T, a.D, false) || !operand(&q.b, a.W_out, a.F, a.D, true) ||
-        !map_of(&q.d[0], ggu, a.T, a.F, 2ull * a.F, 32) || !map_of(&q.d[1], ggu + a.F, a.T, a.F, 2ull * a.F, 32) ||
-        !map_of(&q.d[2], a.h, a.T, a.F, a.F, 32))
+        !map_of(&q.d[0], ggu, a.T, a.F, 2ull * a.F, 32, 32) || !map_of(&q.d[1], ggu + a.F, a.T, a.F, 2ull * a.F, 32, 32) ||
+        !map_of(&q.d[2], a.h, a.T, a.F, a.F, 32, 32))
         return cudaErrorInvalidValue;
     cudaError_t e = run_ffn_any<EPI_GLU_BWD>(prm, st);
     if (e != cudaSuccess) return e;
