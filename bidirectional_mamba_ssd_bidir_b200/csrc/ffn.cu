@@ -73,7 +73,7 @@ struct FfnProb {
 };
 struct FfnParams {
     FfnProb p[kFMaxProb];
-    int nprob, ntiles, save, gelu;
+    int nprob, ntiles, save, gelu, wait_prior;
     const __nv_bfloat16 *gu;       // EPI_GLU_BWD: [M][2N]
     int *status;
     long long wait_cycles;
@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kFfnThreads<EPI>, 1) k_ffn(const __grid_consta
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
     const int first = blockIdx.x / CG, step = gridDim.x / CG;
     const uint32_t MASK = 0xffffffffu;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
@@ -210,6 +211,10 @@ __global__ void __launch_bounds__(kFfnThreads<EPI>, 1) k_ffn(const __grid_consta
         if (lane == 0) {
             long long g = 0;
             bool ok = true;
+            if (prm.wait_prior) {                     // the launch before wrote the operands
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                asm volatile("fence.proxy.async;" ::: "memory");
+            }
             for (int t = first; t < prm.ntiles && ok; t += step) {
                 const FfnWhere w = tile_at<CG>(prm, t, kTileN);
                 const FfnProb &q = prm.p[w.p];
@@ -687,17 +692,19 @@ template <int EPI, int CG> cudaError_t run_ffn(FfnParams &prm, cudaStream_t st) 
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     const int groups = prm.ntiles < sms / CG ? prm.ntiles : sms / CG;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = CG;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(groups * CG);
     cfg.blockDim = dim3(kFfnThreads<EPI>);
     cfg.dynamicSmemBytes = FfnTile<EPI, CG>::kSmem;
     cfg.stream = st;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = prm.wait_prior ? 2 : 1;            // set up while the launch before ends
     return cudaLaunchKernelEx(&cfg, kernel, prm);
 }
 
@@ -790,6 +797,7 @@ cudaError_t launch_ffn(const FfnArgs &a, cudaStream_t st) {
     if (!ok) return cudaErrorInvalidValue;
     cudaError_t e = run_ffn_any<EPI_GLU>(prm, st);
     if (e != cudaSuccess) return e;
+    prm.wait_prior = 1;
     q = product(a.T, a.D, a.F, false, false);
     if (!operand(&q.a, a.h, a.T, a.F, false) || !operand(&q.b, a.W_out, a.D, a.F, false) || !map_of(&q.d[0], a.out, a.T, a.D, a.D, 32))
         return cudaErrorInvalidValue;
@@ -813,6 +821,7 @@ cudaError_t launch_ffn_bwd(const FfnArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     // the longest products first: their tiles end last otherwise
     prm.nprob = 3;
+    prm.wait_prior = 1;
     prm.p[0] = product(a.T, a.D, 2 * a.F, false, true);
     prm.p[1] = product(2 * a.F, a.D, a.T, true, true);
     prm.p[2] = product(a.D, a.F, a.T, true, true);

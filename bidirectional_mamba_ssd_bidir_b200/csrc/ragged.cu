@@ -25,7 +25,7 @@ constexpr int kThreads = 128, kTB = 16;   // threads of a CTA; tokens staged at 
 template <typename T, int P, int N, bool STATES>
 __global__ void __launch_bounds__(kThreads) k_ragged(const __grid_constant__ RaggedArgs a) {
     constexpr int PPT = P / 16, NPT = N / 8, W = NPT < 4 ? NPT : 4, NQ = NPT / W;
-    __shared__ float sx[kTB][P], sB[kTB][N], sC[kTB][N], sy[kTB][P], sdt[kTB], sdec[kTB];
+    __shared__ float sx[kTB][P], sB[kTB][N], sC[kTB][N], sy[kTB][P], sdt[kTB], slog[kTB], sdec[kTB];
     const int u = blockIdx.x, h = blockIdx.y, g = h / (a.H / a.G);
     const Segment sg = find_segment(a.seq, a.seg, u);
     if (u == 0 && h == 0 && !STATES) check_offsets(a.seq, a.status);
@@ -92,12 +92,13 @@ __global__ void __launch_bounds__(kThreads) k_ragged(const __grid_constant__ Rag
             float d = to_f<T>(dt[(first + a.dir * (long long)(b0 + tid)) * a.lddt]);
             if (a.dt_bias) d = softplus(d + bias);
             sdt[tid] = d;
-            sdec[tid] = d * A;
+            slog[tid] = d * A;
+            sdec[tid] = expf(d * A);
         }
         __syncthreads();
-        for (int i = 0; i < m; ++i) {
-            const float d = sdt[i], dec = expf(sdec[i]);
-            total += sdec[i];
+        auto token = [&](int i) {
+            const float d = sdt[i], dec = sdec[i];
+            total += slog[i];
             float xd[PPT], acc[PPT];
 #pragma unroll
             for (int p = 0; p < PPT; ++p) {
@@ -124,6 +125,13 @@ __global__ void __launch_bounds__(kThreads) k_ragged(const __grid_constant__ Rag
                     if (nl == 0) sy[i][PPT * pg + p] = fmaf(Dh, sx[i][PPT * pg + p], acc[p]);
                 }
             }
+        };
+        // only S ties a token to the one before: four at a time hide the loads and the reductions
+        if (m == kTB) {
+#pragma unroll 4
+            for (int i = 0; i < kTB; ++i) token(i);
+        } else {
+            for (int i = 0; i < m; ++i) token(i);
         }
         if (!STATES) {
             __syncthreads();

@@ -67,7 +67,7 @@ struct StepArgs {
 };
 cudaError_t launch_step(const StepArgs &a, bool bf16, cudaStream_t st);
 
-constexpr int kRaggedTable = 712;   // floats of a chunk and head's decay table (ragged_tc.cu)
+constexpr int kRaggedTable = 840;   // floats of a chunk and head's decay table (ragged_tc.cu)
 
 struct RaggedArgs {
     Packed seq;
@@ -120,12 +120,15 @@ __device__ __forceinline__ int seq_find(const Packed &s, int t) {
 struct Segment {
     int s, k, count, lo, len;
 };
+// Called by whole warps: 32 starts are looked at together (a search one by one is a chain of loads, and a
+// kernel's first loads wait for it).
 __device__ __forceinline__ Segment find_segment(const Packed &q, int seg, int u) {
-    int lo = -1, hi = q.nseq;                 // start(lo) / seg + lo <= u < start(hi) / seg + hi
-    while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (seq_start(q, m) / seg + m <= u) lo = m;
-        else hi = m;
+    const int lane = threadIdx.x & 31;
+    int lo = -1;                              // the last sequence with start / seg + number <= u
+    for (int b = 0; b < q.nseq; b += 32) {
+        const int n = __popc(__ballot_sync(0xffffffffu, b + lane < q.nseq && seq_start(q, b + lane) / seg + b + lane <= u));
+        lo += n;
+        if (n < 32) break;
     }
     Segment r{-1, 0, 0, 0, 0};
     if (lo < 0) return r;
@@ -133,7 +136,7 @@ __device__ __forceinline__ Segment find_segment(const Packed &q, int seg, int u)
     r.len = max(0, seq_start(q, lo + 1) - r.lo);
     r.k = u - (r.lo / seg + lo);
     r.count = max(1, (r.len + seg - 1) / seg);
-    r.s = r.k < r.count ? lo : -1;
+    r.s = r.k >= 0 && r.k < r.count ? lo : -1;
     return r;
 }
 

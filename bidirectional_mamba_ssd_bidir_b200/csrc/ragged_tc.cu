@@ -7,7 +7,7 @@
 //
 //   scores    = C B^T, masked to j not after i                     both heads share them
 //   w_j       = dt_j exp(m - cs_j),  rho_i = exp(cs_i - m)
-//   y_i       = rho_i (scores (w x))_i + exp(cs_i) C_i S^T + D x_i
+//   y_i       = rho_i (scores (w x) + C (exp(m) S)^T)_i + D x_i
 //   S        <- exp(c) S + exp(c - m) sum_j (w_j x_j) (outer) B_j
 //
 // With m = c / 2 the exponents of w and rho stay within half the chunk's decay: no factor of the decay
@@ -22,12 +22,14 @@
 // registers in float32.
 //
 // Products (M = 128 each, float32 in TMEM):
-//   scores [0,128)     A = C, B = B tile, both K-major in smem
-//   P X    [256,384)   A = P (bf16, in TMEM over the scores: 32 columns of scores become 16 of P, or in
-//                      the long form 16 of each head's, so a warp overwrites only what it has read),
-//                      B = high of w x (MN-major), N = 128; long form: B = x of a head, N = 64 each
-//   C S^T  [384,512)   A = C, B = bf16 S of both heads (MN-major: row n, 128 columns (head, p))
-//   new S  [128,256)   A = B^T (MN-major, M = n), B = w x high, then rest (MN-major), N = 128
+//   scores    [0,128)    A = C, B = B tile, both K-major in smem
+//   y         [256,512)  two buffers, chunk j in number j & 1: D x / rho, stored there before; then
+//                        A = C, B = bf16 exp(m) S of both heads (MN-major: row n, 128 columns (head, p));
+//                        then A = P (bf16, in TMEM over the scores: 32 columns of scores become 16 of P),
+//                        B = high of w x (MN-major), N = 128.  y = rho (the sum).
+//   new S     [128,256)  A = B^T (MN-major, M = n), B = w x high, then rest (MN-major), N = 128
+// In the long form C S^T, with S as it is, goes to the other buffer of y, 16 columns of each head's P
+// take the place of 32 of scores, and P x is formed a head at a time, N = 64.
 //
 // The long form's P.  It is cut into 32 x 32 blocks; with b the last token before row block I,
 // exp(cs_i - cs_j) dt_j = r_i q_j, r_i = exp(cs_i - cs_b), q_j = exp(cs_b - cs_j) dt_j.  P holds scores_ij q_j,
@@ -40,8 +42,9 @@
 // Warps: 0-7 make P and y, 8-15 the state and w x (TMEM lane quarter w & 3; w >> 2 & 1: two of P's four
 // column blocks, or the head), 16 the TMA loads, 17 to 19 the MMAs: an MMA of N = 128 runs for 32 cycles
 // but takes a thread some 100 to issue, so one issuing warp for the 48 of a chunk would bound it.
-// The two groups run at their own pace.  Group one: P_j, then y_j.  Group two: S from the product of
-// chunk j, w x of chunk j + 1, the bf16 copy of S for chunk j + 1.  Registers: a state warp holds 64
+// The two groups run at their own pace.  Group one: P_j, then y of the chunk before, so that the
+// products of chunk j run meanwhile.  Group two: S from the product of chunk j, its bf16 copy for chunk
+// j + 1, D x / rho of chunk j + 1, and, once P X of chunk j has read w x, w x of chunk j + 1.  Registers: a state warp holds 64
 // columns of S, so the groups are given 88 and 120 a thread and the last warpgroup 56
 // (128 (2 x 88 + 2 x 120 + 56) = 60416 of the 61440 launched with).
 //
@@ -68,32 +71,32 @@ constexpr uint32_t kBox = 128 * 128;                   // 128 rows of 64 bf16: 1
 constexpr int kGroup = 8;                              // warps of a group
 
 // shared memory: everything but the tables in 16 KB boxes; 227 KB in all
-constexpr uint32_t kSX = 0;                            // x: two stages of two heads; becomes y
+constexpr uint32_t kSX = 0;                            // x of two heads (STATES: a second stage where C is otherwise)
 constexpr uint32_t kSW = 4 * kBox;                     // w x: high of two heads, rest of two heads
-constexpr uint32_t kSB = 8 * kBox, kSC = 10 * kBox;    // B, C: two 64-column boxes each
+constexpr uint32_t kSB = 8 * kBox, kSB1 = 2 * kBox, kSC = 10 * kBox;   // B (two stages), C: two 64-column boxes each
 constexpr uint32_t kSS = 12 * kBox;                    // bf16 S: rows n, a box per head
 // One chunk and head's table: the column factors, which every warp reads (copied to shared memory):
 // q of the diagonal blocks, then of row blocks 1, 2, 3 (32, 64 and 96 columns); cs_b of the row blocks,
 // the chunk's decay, the steep blocks' bits,
 // m, and whether the pair takes the short form.  Then per-row values.
 constexpr int kTabQd = 0, kTabQ = 128, kTabRef = 320, kTabTot = 324, kTabSteep = 325, kTabM = 326, kTabShort = 327, kTabShared = 328;
-constexpr int kTabCs = 328, kTabW = 456, kTabCsd = 584, kTabLen = 712;
+constexpr int kTabRho = 328, kTabW = 456, kTabCs = 584, kTabCsd = 712, kTabLen = 840;   // kTabRho: log2 rho
 constexpr float kSteepBlock = 60.f, kSteepChunk = 150.f;
 static_assert(kTabLen == kRaggedTable, "");
 constexpr uint32_t kTab = 14 * kBox;                   // q of both heads
 constexpr uint32_t kBars = kTab + 2 * kTabShared * 4;
 enum TcBar {
-    XF0 = 0, XF1, XE0, XE1, BF, BE, CF, CE, TF,        // loads: full / empty; the tables
-    PREP,                                              // chunk's w x written
-    SC, ST, YI, YF,                                    // products done: scores, new S, C S^T, P X
-    PR, SB, YE,                                        // P written; bf16 S written; Y read
+    XF = 0, XF1, XE, XE1, BF, BF1, BE, BE1, CF, CE, TF, // loads: full / empty (x: two stages in STATES only); tables
+    PREP, PREP1,                                       // w x written (even and odd chunks)
+    SC, ST, ST1, YI, YF0, YF1,                         // products done: scores, new S (even and odd), C S^T, y (by buffer)
+    PR, PR1, SB, YB, YE0, YE1,                         // P written; S's copy; D x / rho; y read (by buffer)
     DONE,
     kNumBars
 };
 constexpr uint32_t kMisc = (kBars + kNumBars * 8 + 15) & ~15u;
 constexpr uint32_t kTcSmem = kMisc + 32;
 static_assert(kTcSmem <= 232448, "shared memory budget");
-constexpr uint32_t kColS = 128, kColY = 256, kColYI = 384;   // TMEM columns (scores / P at 0)
+constexpr uint32_t kColS = 128, kColY = 256;           // TMEM columns (scores / P at 0; y: two buffers of 128)
 
 // Chunk number of the j-th chunk of sequence s: as the segments are numbered (ragged.cu), with chunks
 // for segments.
@@ -107,6 +110,7 @@ __global__ void __launch_bounds__(kTabThreads) k_ragged_tables(const __grid_cons
     __shared__ float d[kTabHeads][kQ + 1], tots[kTabHeads];
     const int c = blockIdx.x, g0 = blockIdx.y * kTabHeads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Segment sg = find_segment(a.seq, kQ, c);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (sg.s < 0 || sg.len == 0) return;
     const int n = min(kQ, sg.len - sg.k * kQ);
     const int base = a.dir > 0 ? sg.lo + sg.k * kQ : sg.lo + sg.len - (sg.k + 1) * kQ;
@@ -164,14 +168,17 @@ __global__ void __launch_bounds__(kTabThreads) k_ragged_tables(const __grid_cons
 #pragma unroll
         for (int k = 0; k < 4; ++k) b[k + 1] = __shfl_sync(0xffffffffu, cs[3], 8 * k + 7);
         const int blk = lane >> 3;
+        const bool steep_own = (blk == 0 ? b[0] - b[1] : blk == 1 ? b[1] - b[2] : blk == 2 ? b[2] - b[3] : b[3] - b[4]) > kSteepBlock;
         const float own = blk == 0 ? b[0] : blk == 1 ? b[1] : blk == 2 ? b[2] : b[3];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int k = 4 * lane + e, row = a.dir > 0 ? k : kQ - 1 - k;      // row of the tile
-            out[kTabCs + row] = cs[e];
-            out[kTabCsd + row] = cs[e] - __log2f(dt[e]);
+            out[kTabRho + row] = small ? cs[e] - m : steep_own ? 0.f : cs[e] - own;
             // (the long form's exponent is the sum itself, not a difference)
             out[kTabW + row] = dt[e] * ex2_ftz(small ? m - cs[e] : ed + dn[e]);
+            if (small) continue;                       // the rest is the long form's
+            out[kTabCs + row] = cs[e];
+            out[kTabCsd + row] = cs[e] - __log2f(dt[e]);
             out[kTabQd + row] = dt[e] * ex2_ftz(own - cs[e]);
 #pragma unroll
             for (int I = 1; I < 4; ++I)
@@ -212,24 +219,29 @@ __device__ __forceinline__ bool elect_one() {
 template <int R> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-constexpr int kTcThreads = 640, kStThreads = 384;      // STATES has no first group of warps
+constexpr int kTcThreads = 640;
 
 template <bool STATES>
-__global__ void __launch_bounds__(STATES ? kStThreads : kTcThreads, 1) k_ragged_tc(const __grid_constant__ TcMaps maps,
+__global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_constant__ TcMaps maps,
                                                              const __grid_constant__ RaggedArgs a) {
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sbase = smem_u32(sm);
     auto bar = [&](int i) { return sbase + kBars + 8u * i; };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + kMisc + 4);
-    const int warp = (threadIdx.x >> 5) + (STATES ? kGroup : 0), lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t MASK = 0xffffffffu;
     const int pairs = a.H / 2, u = blockIdx.x / pairs, h0 = 2 * (blockIdx.x % pairs), grp = h0 / (a.H / a.G);
+    // The launches of a call follow one another with programmatic dependent launch; what this one reads of
+    // the ones before, it reads behind the wait.  (Every CTA waits, so that the next launch's wait covers all.)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Segment sg = find_segment(a.seq, a.seg, u);
     if (blockIdx.x == 0 && !STATES) check_offsets(a.seq, a.status);
-    if (sg.s < 0) return;                              // the same for the whole CTA, before any allocation
     const bool last = sg.k == sg.count - 1;
-    if (STATES && last) return;
+    if (sg.s < 0 || (STATES && last)) {                // the same for the whole CTA, before any allocation
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     if (sbase & 1023) {                                // the swizzled boxes need it (never seen)
         if (threadIdx.x == 0) atomicExch(a.status, 150);
         return;
@@ -244,8 +256,8 @@ __global__ void __launch_bounds__(STATES ? kStThreads : kTcThreads, 1) k_ragged_
         *abort_flag = 0;
         *reinterpret_cast<volatile long long *>(abort_flag + 1) = a.wait_cycles;
         for (int i = 0; i < kNumBars; ++i) {
-            const bool group = i == PREP || i == PR || i == SB || i == YE || i == XE0 || i == XE1;
-            mbar_init(bar(i), group ? kGroup : i == DONE ? 3 : (i == BE && !STATES) ? 2 : 1);
+            const bool group = i == PR || i == PR1 || i == SB || i == YB || i == YE0 || i == YE1;
+            mbar_init(bar(i), (i == PREP || i == PREP1 || i == XE || i == XE1) ? 2 * kGroup : group ? kGroup : i == DONE ? 3 : ((i == BE || i == BE1) && !STATES) ? 2 : 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -256,24 +268,74 @@ __global__ void __launch_bounds__(STATES ? kStThreads : kTcThreads, 1) k_ragged_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t tmem = *tmem_slot;
     auto wait = [&](int b, int phase, int code) { return mbar_wait(bar(b), (uint32_t)phase & 1, MASK, abort_flag, a.status, code); };
 
-    if (!STATES && warp >= 16) regs_down<56>();
+    // w x of chunk j in two bf16 terms: this thread's row, 32 of the head's columns; rows of no token zero
+    auto weigh = [&](int j, int row, int hh, int side, float w) {
+        const int n = rows(j);
+        const bool mine = a.dir > 0 ? row < n : row >= kQ - n;
+        const uint8_t *x = sm + (STATES && j & 1 ? kSC : kSX) + hh * kBox;
+        uint8_t *to = sm + kSW + hh * kBox;
+        const float2 w2 = make_float2(w, w), m1 = make_float2(-1.f, -1.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t off = swz(row, 4 * side + i);
+            uint4 v = *reinterpret_cast<const uint4 *>(x + off);
+            if (!mine) v = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = mul2(unpack2(in[e]), w2);
+                hi[e] = pack_bf16(f.x, f.y);
+                const float2 rest = fma2(unpack2(hi[e]), m1, f);
+                lo[e] = pack_bf16(rest.x, rest.y);
+            }
+            *reinterpret_cast<uint4 *>(to + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4 *>(to + 2 * kBox + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_async_smem();
+        __syncwarp();
+    };
+    // STATES, group one: its half of w x
+    auto side_states = [&]() {
+        const int row = 32 * (warp & 3) + lane, hh = warp >> 2;
+        const float *t = a.tables + ((size_t)chunk0 * a.H + h0 + hh) * kTabLen + kTabW + row;
+        float w = nc > 0 ? *t : 0.f;
+        for (int j = 0; j < nc; ++j) {
+            const float now = w;
+            t += (size_t)a.H * kTabLen;
+            if (j + 1 < nc) w = *t;
+            // the product of the chunk before has read w x
+            if (!wait(XF + (j & 1), j >> 1, 191) || (j >= 1 && !wait(ST + ((j - 1) & 1), (j - 1) >> 1, 192))) break;
+            weigh(j, row, hh, 1, now);
+            if (lane == 0) {
+                mbar_arrive(bar(PREP + (j & 1)));
+                mbar_arrive(bar(XE + (j & 1)));
+            }
+        }
+    };
+    if (warp >= 16) regs_down<56>();
     if (warp == 16) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
             auto wait1 = [&](int b, int phase, int code) { return mbar_wait(bar(b), (uint32_t)phase & 1, 1u, abort_flag, a.status, code); };
-            int nx = 0, nb = 0, ncc = 0, nt = 0;       // chunks asked for
+            int nx = 0, nb = 0, ncc = 0, nt = 0;       // chunks asked for (nt: tables, of long chunks alone)
+            const float *tg = a.tables + ((size_t)chunk0 * a.H + h0) * kTabLen + kTabShort;
+            float next = nc > 0 ? *tg : 0.f;
             for (int j = 0; j < nc; ++j) {
-                const int r = base(j), st = j & 1;
-                if (j >= 2 && !wait1(XE0 + st, (j >> 1) - 1, 151)) break;
-                mbar_expect_tx(bar(XF0 + st), 2 * kBox);
-                for (int h = 0; h < 2; ++h) tma_load_2d(sbase + kSX + (2 * st + h) * kBox, &maps.x, 64 * (h0 + h), r, bar(XF0 + st));
+                const int r = base(j);
+                const int st = STATES ? j & 1 : 0;
+                if (STATES ? j >= 2 && !wait1(XE + st, (j >> 1) - 1, 151) : j >= 1 && !wait1(XE, j - 1, 151)) break;
+                mbar_expect_tx(bar(XF + st), 2 * kBox);
+                for (int h = 0; h < 2; ++h) tma_load_2d(sbase + (st ? kSC : kSX) + h * kBox, &maps.x, 64 * (h0 + h), r, bar(XF + st));
                 nx = j + 1;
-                if (j >= 1 && !wait1(BE, j - 1, 152)) break;
-                mbar_expect_tx(bar(BF), 2 * kBox);
-                for (int h = 0; h < 2; ++h) tma_load_2d(sbase + kSB + h * kBox, &maps.b, 128 * grp + 64 * h, r, bar(BF));
+                if (j >= 2 && !wait1(BE + (j & 1), (j >> 1) - 1, 152)) break;
+                mbar_expect_tx(bar(BF + (j & 1)), 2 * kBox);
+                for (int h = 0; h < 2; ++h)
+                    tma_load_2d(sbase + (j & 1 ? kSB1 : kSB) + h * kBox, &maps.b, 128 * grp + 64 * h, r, bar(BF + (j & 1)));
                 nb = j + 1;
                 if (STATES) continue;
                 if (j >= 1 && !wait1(CE, j - 1, 153)) break;
@@ -285,17 +347,22 @@ __global__ void __launch_bounds__(STATES ? kStThreads : kTcThreads, 1) k_ragged_
                     for (int h = 0; h < 2; ++h) tma_prefetch_2d(&maps.b, 128 * grp + 64 * h, base(j + 2));
                     for (int h = 0; h < 2; ++h) tma_prefetch_2d(&maps.c, 128 * grp + 64 * h, base(j + 2));
                 }
-                // the tables of the chunk before are read by its P pass
-                if (j >= 1 && !wait1(PR, j - 1, 162)) break;
+                // the factors of the long form's P, once the P pass before has read its own
+                if (j >= 1 && !wait1(PR + ((j - 1) & 1), (j - 1) >> 1, 162)) break;
+                const bool small = next != 0.f;
+                tg += (size_t)a.H * kTabLen;
+                if (j + 1 < nc) next = *tg;
+                if (small) continue;
                 mbar_expect_tx(bar(TF), 2 * kTabShared * 4);
                 for (int h = 0; h < 2; ++h)
                     bulk_load(sbase + kTab + h * kTabShared * 4, a.tables + ((size_t)(chunk0 + j) * a.H + h0 + h) * kTabLen,
                               kTabShared * 4, bar(TF));
-                nt = j + 1;
+                ++nt;
             }
             if (*abort_flag) {                         // copies in flight land before the memory is given up
-                for (int j = nx - 1; j >= 0 && j >= nx - 2; --j) mbar_drain(bar(XF0 + (j & 1)), (uint32_t)(j >> 1) & 1, a.wait_cycles);
-                if (nb) mbar_drain(bar(BF), (uint32_t)(nb - 1) & 1, a.wait_cycles);
+                for (int j = nx - 1; j >= 0 && j >= nx - (STATES ? 2 : 1); --j)
+                    mbar_drain(bar(XF + (STATES ? j & 1 : 0)), (uint32_t)(STATES ? j >> 1 : j) & 1, a.wait_cycles);
+                for (int j = nb - 1; j >= 0 && j >= nb - 2; --j) mbar_drain(bar(BF + (j & 1)), (uint32_t)(j >> 1) & 1, a.wait_cycles);
                 if (ncc) mbar_drain(bar(CF), (uint32_t)(ncc - 1) & 1, a.wait_cycles);
                 if (nt) mbar_drain(bar(TF), (uint32_t)(nt - 1) & 1, a.wait_cycles);
             }
@@ -305,14 +372,20 @@ __global__ void __launch_bounds__(STATES ? kStThreads : kTcThreads, 1) k_ragged_
         // ------------------------------------------------------------ products that read C: scores, C S^T
         if (!STATES) {
             const uint32_t id_sc = idesc(128, 0, 0), id_yi = idesc(128, 0, 1);
-            const SDesc dC = make_sdesc(sbase + kSC, 16, 1024), dBk = make_sdesc(sbase + kSB, 16, 1024), dS = make_sdesc(sbase + kSS, kBox, 1024);
+            const SDesc dC = make_sdesc(sbase + kSC, 16, 1024), dB0 = make_sdesc(sbase + kSB, 16, 1024), dB1 = make_sdesc(sbase + kSB1, 16, 1024), dS = make_sdesc(sbase + kSS, kBox, 1024);
+            const float *tg = a.tables + ((size_t)chunk0 * a.H + h0) * kTabLen + kTabShort;
+            float next = nc > 0 ? *tg : 0.f;
             for (int j = 0; j < nc; ++j) {
-                // P of the chunk before lies over the scores until P X has read it; a partial chunk's B
-                // is zeroed in part first
-                if (!wait(BF, j, 155) || !wait(CF, j, 157) || (j >= 1 && !wait(YF, j - 1, 156)) || (rows(j) < kQ && !wait(PREP, j, 154)))
+                const bool small = next != 0.f;
+                tg += (size_t)a.H * kTabLen;
+                if (j + 1 < nc) next = *tg;
+                // P of the chunk before lies over the scores until its product has read it; a partial
+                // chunk's B is zeroed in part first
+                const SDesc dBk = j & 1 ? dB1 : dB0;
+                if (!wait(BF + (j & 1), j >> 1, 155) || !wait(CF, j, 157) || (j >= 1 && !wait(YF0 + ((j - 1) & 1), (j - 1) >> 1, 156)) ||
+                    (rows(j) < kQ && !wait(PREP + (j & 1), j >> 1, 154)))
                     break;
                 tc_fence_after();
-                // K = n: 64 of them to a box, 16 to a step of 32 bytes
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
@@ -320,15 +393,17 @@ __global__ void __launch_bounds__(STATES ? kStThreads : kTcThreads, 1) k_ragged_
                         mma_ss(tmem, dC.at(off), dBk.at(off), id_sc, ks > 0);
                     }
                     mma_commit(bar(SC));
-                    mma_commit(bar(BE));
+                    mma_commit(bar(BE + (j & 1)));
                 }
                 __syncwarp();
-                if (!wait(SB, j, 158) || (j >= 1 && !wait(YE, j - 1, 159))) break;
+                // (the long form's goes into the other buffer, once the y before has been read there)
+                if (!wait(SB, j, 158) || !wait(YB, j, 150) || (!small && j >= 1 && !wait(YE0 + ((j - 1) & 1), (j - 1) >> 1, 159))) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        mma_ss(tmem + kColYI, dC.at((ks >> 2) * kBox + (ks & 3) * 32), dS.at(ks * 2048), id_yi, ks > 0);
+                        mma_ss(tmem + kColY + 128 * (small ? j & 1 : (j & 1) ^ 1), dC.at((ks >> 2) * kBox + (ks & 3) * 32), dS.at(ks * 2048), id_yi,
+                               small || ks > 0);
                     mma_commit(bar(YI));
                     mma_commit(bar(CE));
                 }
@@ -341,16 +416,17 @@ __global__ void __launch_bounds__(STATES ? kStThreads : kTcThreads, 1) k_ragged_
     } else if (warp == 18) {
         // ------------------------------------------------------------ the product of the state (K = tokens: 16 rows of 128 bytes to a step)
         const uint32_t id_st = idesc(128, 1, 1);
-        const SDesc dBm = make_sdesc(sbase + kSB, kBox, 1024), dW = make_sdesc(sbase + kSW, kBox, 1024);
+        const SDesc dB0 = make_sdesc(sbase + kSB, kBox, 1024), dB1 = make_sdesc(sbase + kSB1, kBox, 1024), dW = make_sdesc(sbase + kSW, kBox, 1024);
         for (int j = 0; j < nc; ++j) {
-            if (!wait(PREP, j, 160) || !wait(BF, j, 172)) break;
+            const SDesc dBm = j & 1 ? dB1 : dB0;
+            if (!wait(PREP + (j & 1), j >> 1, 160) || !wait(BF + (j & 1), j >> 1, 172)) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
                 for (int ks = 0; ks < 16; ++ks)
                     mma_ss(tmem + kColS, dBm.at((ks & 7) * 2048), dW.at((ks >> 3) * 2 * kBox + (ks & 7) * 2048), id_st, ks > 0);
-                mma_commit(bar(ST));
-                mma_commit(bar(BE));
+                mma_commit(bar(ST + (j & 1)));
+                mma_commit(bar(BE + (j & 1)));
             }
             __syncwarp();
         }
@@ -361,30 +437,29 @@ __global__ void __launch_bounds__(STATES ? kStThreads : kTcThreads, 1) k_ragged_
         // ------------------------------------------------------------ P X
         if (!STATES) {
             const uint32_t id_px = idesc(64, 0, 1), id_pw = idesc(128, 0, 1);
-            const SDesc dW = make_sdesc(sbase + kSW, kBox, 1024);
+            const SDesc dX = make_sdesc(sbase + kSX, kBox, 1024), dW = make_sdesc(sbase + kSW, kBox, 1024);
             const float *tg = a.tables + ((size_t)chunk0 * a.H + h0) * kTabLen + kTabShort;
             float next = nc > 0 ? *tg : 0.f;
-            const SDesc dX0 = make_sdesc(sbase + kSX, kBox, 1024), dX1 = make_sdesc(sbase + kSX + 2 * kBox, kBox, 1024);
             for (int j = 0; j < nc; ++j) {
                 const bool small = next != 0.f;
                 tg += (size_t)a.H * kTabLen;
                 if (j + 1 < nc) next = *tg;
-                if (!wait(XF0 + (j & 1), j >> 1, 173) || !wait(PREP, j, 174) || !wait(PR, j, 175)) break;
+                // in the short form C S^T lies under it: another thread's products, so they are waited for
+                if (!wait(PREP + (j & 1), j >> 1, 174) || !wait(PR + (j & 1), j >> 1, 175) || !wait(YI, j, 177)) break;
                 tc_fence_after();
-                const SDesc dX = j & 1 ? dX1 : dX0;
+                const uint32_t y = tmem + kColY + 128 * (j & 1);
                 if (small) {
                     if (elect_one()) {
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            mma_ts(tmem + kColY, tmem + 32 * (ks >> 1) + 8 * (ks & 1), dW.at(ks * 2048), id_pw, ks > 0);
-                        mma_commit(bar(YF));
+                        for (int ks = 0; ks < 8; ++ks) mma_ts(y, tmem + 32 * (ks >> 1) + 8 * (ks & 1), dW.at(ks * 2048), id_pw, 1);
+                        mma_commit(bar(YF0 + (j & 1)));
                     }
                 } else if (elect_one()) {
 #pragma unroll
                     for (int ks = 0; ks < 16; ++ks)
-                        mma_ts(tmem + kColY + 64 * (ks >> 3), tmem + 32 * (ks >> 1 & 3) + 16 * (ks >> 3) + 8 * (ks & 1),
-                               dX.at((ks >> 3) * kBox + (ks & 7) * 2048), id_px, (ks & 7) > 0);
-                    mma_commit(bar(YF));
+                        mma_ts(y + 64 * (ks >> 3), tmem + 32 * (ks >> 1 & 3) + 16 * (ks >> 3) + 8 * (ks & 1),
+                               dX.at((ks >> 3) * kBox + (ks & 7) * 2048), id_px, 1);
+                    mma_commit(bar(YF0 + (j & 1)));
                 }
                 __syncwarp();
             }
@@ -394,36 +469,32 @@ __global__ void __launch_bounds__(STATES ? kStThreads : kTcThreads, 1) k_ragged_
         __syncwarp();
     } else if (warp < kGroup) {
         // ------------------------------------------------------------ P and y
-        if constexpr (!STATES) {
-            regs_down<88>();
+        regs_down<88>();
+        if constexpr (STATES) {
+            side_states();
+        } else {
             const int q = warp & 3, hh = warp >> 2, h = h0 + hh, row = 32 * q + lane;
             const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
             const float *tab = reinterpret_cast<const float *>(sm + kTab);
-            const float Dh = a.D ? a.D[h] : 0.f;
             const int rb = a.dir > 0 ? q : 3 - q;      // scan number of the row block
-            const float *tg = a.tables + ((size_t)chunk0 * a.H + h0) * kTabLen;   // chunk j's: j a.H kTabLen on
-            float n0 = 0.f, n1 = 0.f;                  // cs of the row and both heads, loaded a chunk ahead
-            if (nc > 0) {
-                n0 = tg[kTabCs + row];
-                n1 = tg[kTabLen + kTabCs + row];
-            }
-            for (int j = 0; j < nc; ++j) {
-                const int st = j & 1;
-                const float cs0 = n0, cs1 = n1;
-                const float *t0p = tg, *t1p = tg + kTabLen;
-                tg += (size_t)a.H * kTabLen;
-                if (j + 1 < nc) {
-                    n0 = tg[kTabCs + row];
-                    n1 = tg[kTabLen + kTabCs + row];
+            const float *tg = a.tables + ((size_t)chunk0 * a.H + h0) * kTabLen;   // chunk 0's; a.H kTabLen on to the next
+            const size_t step = (size_t)a.H * kTabLen;
+            // ---- P_j: this thread's row, column blocks 2 hh and 2 hh + 1
+            int longs = 0;                             // chunks of the long form so far
+            auto make_p = [&](int j, bool small) -> bool {
+                if (!small && !wait(TF, longs++, 165)) return false;
+                const float *u0 = tab, *u1 = tab + kTabShared, *t0p = tg + j * step, *t1p = t0p + kTabLen;
+                float cs0 = 0.f, cs1 = 0.f, rf0 = 1.f, rf1 = 1.f;
+                bool steep0 = false, steep1 = false;
+                if (!small) {
+                    cs0 = t0p[kTabCs + row];
+                    cs1 = t1p[kTabCs + row];
+                    rf0 = ex2_ftz(cs0 - u0[kTabRef + rb]);
+                    rf1 = ex2_ftz(cs1 - u1[kTabRef + rb]);
+                    steep0 = __float_as_int(u0[kTabSteep]) >> rb & 1;
+                    steep1 = __float_as_int(u1[kTabSteep]) >> rb & 1;
                 }
-                if (!wait(TF, j, 165)) break;
-                const float *u0 = tab, *u1 = tab + kTabShared;
-                const bool small = u0[kTabShort] != 0.f;
-                const float rf0 = ex2_ftz(cs0 - u0[kTabRef + rb]), rf1 = ex2_ftz(cs1 - u1[kTabRef + rb]);
-                const bool steep0 = __float_as_int(u0[kTabSteep]) >> rb & 1, steep1 = __float_as_int(u1[kTabSteep]) >> rb & 1;
-                const float ecs = ex2_ftz(hh ? cs1 : cs0), ry = small ? ex2_ftz(hh ? cs1 - u1[kTabM] : cs0 - u0[kTabM]) : hh ? (steep1 ? 1.f : rf1) : (steep0 ? 1.f : rf0);
-                // ---- P_j: this thread's row, column blocks 2 hh and 2 hh + 1
-                if (!wait(SC, j, 166)) break;
+                if (!wait(SC, j, 166)) return false;
                 tc_fence_after();
 #pragma unroll 1
                 for (int x = 0; x < 2; ++x) {
@@ -495,58 +566,116 @@ __global__ void __launch_bounds__(STATES ? kStThreads : kTcThreads, 1) k_ragged_
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(PR));
-                // ---- y_j, in place over x_j: this thread's row of head h
-                if (!wait(YI, j, 170) || !wait(YF, j, 171)) break;
+                if (lane == 0) mbar_arrive(bar(PR + (j & 1)));
+                return true;
+            };
+            // ---- y_j: this thread's row of head h
+            auto make_y = [&](int j, bool small, float lr, float cs) -> bool {
+                const int buf = j & 1;
+                if (!wait(YF0 + buf, j >> 1, 171) || (!small && !wait(YI, j, 170))) return false;
                 tc_fence_after();
-                uint8_t *box = sm + kSX + (2 * st + hh) * kBox;
-                const float2 e2 = make_float2(ecs, ecs), d2 = make_float2(Dh, Dh), r2 = make_float2(ry, ry);
+                const float rho = ex2_ftz(lr), ecs = ex2_ftz(cs);
+                const float2 r2 = make_float2(rho, rho), e2 = make_float2(ecs, ecs);
+                const int n = rows(j), r0 = row & ~1;
+                const bool even_in = a.dir > 0 ? r0 < n : r0 >= kQ - n, odd_in = a.dir > 0 ? r0 + 1 < n : r0 + 1 >= kQ - n;
+                __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + (long long)(base(j) + r0) * a.ldy + h * 64;
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    float yp[16], yi[16];
-                    tmem_ld16(tl + kColY + 64 * hh + 16 * z, yp);
-                    tmem_ld16(tl + kColYI + 64 * hh + 16 * z, yi);
-                    if (z == 3) {
+                for (int z = 0; z < 2; ++z) {
+                    float v[32];
+                    tmem_ld32(tl + kColY + 128 * buf + 64 * hh + 32 * z, v);
+                    if (small) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 t = mul2(make_float2(v[i], v[i + 1]), r2);
+                            v[i] = t.x;
+                            v[i + 1] = t.y;
+                        }
+                    } else {
+                        float yi[32];
+                        tmem_ld32(tl + kColY + 128 * (buf ^ 1) + 64 * hh + 32 * z, yi);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) {
+                            const float2 t = fma2(make_float2(yi[i], yi[i + 1]), e2, mul2(make_float2(v[i], v[i + 1]), r2));
+                            v[i] = t.x;
+                            v[i + 1] = t.y;
+                        }
+                    }
+                    if (z == 1) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(YE));
+                        if (lane == 0) mbar_arrive(bar(YE0 + buf));
                     }
+                    // 16 bytes of a row a lane, but whole sectors of 32 are stored: neighbouring lanes trade
+                    // halves, so that each pair stores 32 bytes of the even row, then of the odd one
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        uint4 *at = reinterpret_cast<uint4 *>(box + swz(row, 2 * z + i));
-                        const uint4 x = *at;
-                        const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-                        uint32_t o[4];
+                        uint32_t p[2][4];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) p[c][e] = pack_bf16(v[16 * i + 8 * c + 2 * e], v[16 * i + 8 * c + 2 * e + 1]);
+                        const bool odd = lane & 1;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int c = 8 * i + 2 * e;
-                            const float2 t = fma2(e2, make_float2(yi[c], yi[c + 1]), mul2(d2, unpack2(in[e])));
-                            const float2 y2 = fma2(r2, make_float2(yp[c], yp[c + 1]), t);
-                            o[e] = pack_bf16(y2.x, y2.y);
+                            const uint32_t got = __shfl_xor_sync(MASK, odd ? p[0][e] : p[1][e], 1);
+                            if (odd) p[0][e] = got;
+                            else p[1][e] = got;
                         }
-                        *at = make_uint4(o[0], o[1], o[2], o[3]);
+                        // now p[0]: this lane's half of the even row's 32 bytes, p[1]: of the odd row's
+                        __nv_bfloat16 *to = y + 32 * z + 16 * i + 8 * (lane & 1);
+                        if (even_in) __stcs(reinterpret_cast<uint4 *>(to), make_uint4(p[0][0], p[0][1], p[0][2], p[0][3]));
+                        if (odd_in) __stcs(reinterpret_cast<uint4 *>(to + a.ldy), make_uint4(p[1][0], p[1][1], p[1][2], p[1][3]));
                     }
                 }
-                // the warp's 32 rows x 128 bytes, eight lanes to a row, rows of the segment only
-                __syncwarp();
-                const int n = rows(j);
-                uint4 o[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = *reinterpret_cast<const uint4 *>(box + swz(32 * q + 4 * i + (lane >> 3), lane & 7));
-                fence_async_smem();                    // the next load of this stage comes after these accesses
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(XE0 + st));
-                __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(a.y) + (long long)(base(j) + 32 * q + (lane >> 3)) * a.ldy + h * 64 + 8 * (lane & 7);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = 32 * q + 4 * i + (lane >> 3);
-                    if (a.dir > 0 ? r < n : r >= kQ - n) __stcs(reinterpret_cast<uint4 *>(y + 4LL * i * a.ldy), o[i]);
+                return true;
+            };
+            // its half of w x of chunk j
+            auto weigh_half = [&](int j, float w, bool small) -> bool {
+                if (!wait(XF, j, 193)) return false;
+                weigh(j, row, hh, 1, w);
+                if (lane == 0) {
+                    mbar_arrive(bar(PREP + (j & 1)));
+                    if (small) mbar_arrive(bar(XE));   // the long form's product reads x itself
                 }
+                return true;
+            };
+            bool was_small = true, ok = true;
+            float lr = 0.f, cs = 0.f;                  // log2 rho and cs of the row, of the chunk before
+            const float *tw = tg + hh * kTabLen;       // own head's table of the chunk
+            float nshort = nc > 0 ? tw[kTabShort] : 1.f;
+            if (nc > 0) ok = weigh_half(0, tw[kTabW + row], nshort != 0.f);
+            for (int j = 0; j <= nc && ok; ++j) {
+                float nlr = 0.f, ncs = 0.f, nw = 0.f;
+                const bool small = nshort != 0.f;
+                if (j + 1 < nc) {
+                    nw = tw[step + kTabW + row];
+                    nshort = tw[step + kTabShort];
+                }
+                tw += step;
+                if (j < nc) {
+                    const float *t = tg + j * step + hh * kTabLen + row;
+                    nlr = t[kTabRho];
+                    ncs = t[kTabCs];                   // (not a number of ours in the short form, which has no use for it)
+                }
+                // after a chunk of the long form its y comes first: it frees both buffers of y, which
+                // what P_j waits for may need
+                if (j >= 1 && !was_small) ok = make_y(j - 1, false, lr, cs);
+                if (ok && j < nc) ok = make_p(j, small);
+                if (ok && j >= 1 && was_small) ok = make_y(j - 1, true, lr, cs);
+                if (ok && j + 1 < nc) {
+                    // both products have read the w x (P X of the long form: the x) of this chunk
+                    if (!(ok = wait(YF0 + (j & 1), j >> 1, 194) && wait(ST + (j & 1), j >> 1, 195))) break;
+                    if (!small && lane == 0) mbar_arrive(bar(XE));
+                    ok = weigh_half(j + 1, nw, nshort != 0.f);
+                }
+                was_small = small;
+                lr = nlr;
+                cs = ncs;
             }
         }
     } else if (warp < 2 * kGroup) {
         // ------------------------------------------------------------ the state and w x
-        if constexpr (!STATES) regs_up<120>();
+        regs_up<120>();
         const int q = warp & 3, hh = warp >> 2 & 1, h = h0 + hh, row = 32 * q + lane;   // n of the state, row of w x
         const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
         const size_t PN = 64 * 128, at = (size_t)h * PN + row;
@@ -580,74 +709,102 @@ __global__ void __launch_bounds__(STATES ? kStThreads : kTcThreads, 1) k_ragged_
                     for (int i = 0; i < 64; ++i) S[i] = fmaf(S[i], d, add[i * 128]);
                 }
         }
-        auto copy_state = [&]() {                      // bf16 S: row n of the head's box
+        // Of the chunk that is next: w and log2 rho of this row, c and m (log2), its form
+        float wr = 0.f, lr = 0.f, tot = 0.f, ref = 0.f, total = 0.f;
+        bool small = false;
+        const float Dh = a.D ? a.D[h] : 0.f;
+        auto load_w = [&](int j) {
+            const float *t = a.tables + ((size_t)(chunk0 + j) * a.H + h) * kTabLen;
+            wr = t[kTabW + row];
+            lr = t[kTabRho + row];
+            tot = t[kTabTot];
+            ref = t[kTabM];
+            small = t[kTabShort] != 0.f;
+        };
+        auto copy_state = [&]() {                      // bf16 exp(m) S (long form: S): row n of the head's box
+            const float f = small ? ex2_ftz(ref) : 1.f;
+            const float2 f2 = make_float2(f, f);
             uint8_t *box = sm + kSS + hh * kBox;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4 *>(box + swz(row, i)) =
-                    make_uint4(pack_bf16(S[8 * i], S[8 * i + 1]), pack_bf16(S[8 * i + 2], S[8 * i + 3]),
-                               pack_bf16(S[8 * i + 4], S[8 * i + 5]), pack_bf16(S[8 * i + 6], S[8 * i + 7]));
+            for (int i = 0; i < 8; ++i) {
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 t = mul2(make_float2(S[8 * i + 2 * e], S[8 * i + 2 * e + 1]), f2);
+                    o[e] = pack_bf16(t.x, t.y);
+                }
+                *reinterpret_cast<uint4 *>(box + swz(row, i)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(SB));
         };
-        float wr = 0.f, tot = 0.f, ref = 0.f, total = 0.f;   // w of this row, c and m (log2) of the chunk prepared last
-        auto load_w = [&](int j) {
-            const float *t = a.tables + ((size_t)(chunk0 + j) * a.H + h) * kTabLen;
-            wr = t[kTabW + row];
-            tot = t[kTabTot];
-            ref = t[kTabM];
-        };
-        // w x of chunk j
-        auto prepare = [&](int j) -> bool {
-            const int st = j & 1, n = rows(j);
-            if (!wait(XF0 + st, j >> 1, 163)) return false;
-            uint8_t *x = sm + kSX + (2 * st + hh) * kBox;
-            if (n < kQ) {                              // rows of no token: zero in x and B
-                if (!wait(BF, j, 164)) return false;
+        uint8_t *xb = sm + kSX + hh * kBox;
+        // chunk j has landed; rows of no token: zero in x (the long form's product reads it) and B
+        auto land = [&](int j) -> bool {
+            if (!wait(XF + (STATES ? j & 1 : 0), STATES ? j >> 1 : j, 163)) return false;
+            const int n = rows(j);
+            if (n < kQ) {
+                if (!wait(BF + (j & 1), j >> 1, 164)) return false;
                 if (a.dir > 0 ? row >= n : row < kQ - n)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        *reinterpret_cast<uint4 *>(x + swz(row, i)) = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4 *>(sm + kSB + hh * kBox + swz(row, i)) = make_uint4(0u, 0u, 0u, 0u);
+                        if (!STATES) *reinterpret_cast<uint4 *>(xb + swz(row, i)) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(sm + (j & 1 ? kSB1 : kSB) + hh * kBox + swz(row, i)) = make_uint4(0u, 0u, 0u, 0u);
                     }
             }
-            const float2 w2 = make_float2(wr, wr), m1 = make_float2(-1.f, -1.f);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t off = swz(row, i);
-                const uint4 v = *reinterpret_cast<const uint4 *>(x + off);
-                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = mul2(unpack2(in[e]), w2);
-                    hi[e] = pack_bf16(f.x, f.y);
-                    const float2 rest = fma2(unpack2(hi[e]), m1, f);
-                    lo[e] = pack_bf16(rest.x, rest.y);
-                }
-                *reinterpret_cast<uint4 *>(sm + kSW + hh * kBox + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(sm + kSW + (2 + hh) * kBox + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(bar(PREP));
-                if (STATES) mbar_arrive(bar(XE0 + st));
-            }
             return true;
+        };
+        // D x / rho of chunk j into its buffer of y
+        auto start_y = [&](int j) {
+            const float f = Dh * ex2_ftz(-lr);
+            const float2 f2 = make_float2(f, f);
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                float v[32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(xb + swz(row, 4 * z + i));
+                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 t = mul2(unpack2(in[e]), f2);
+                        v[8 * i + 2 * e] = t.x;
+                        v[8 * i + 2 * e + 1] = t.y;
+                    }
+                }
+                tmem_st32f_nw(tl + kColY + 128 * (j & 1) + 64 * hh + 32 * z, v);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(YB));
+        };
+        // its half of w x of chunk j
+        auto prepare = [&](int j) {
+            weigh(j, row, hh, 0, wr);
+            if (lane == 0) {
+                mbar_arrive(bar(PREP + (j & 1)));
+                if (STATES) mbar_arrive(bar(XE + (j & 1)));
+                else if (small) mbar_arrive(bar(XE));  // the long form's product reads x itself
+            }
         };
         bool ok = true;
         if (nc > 0) {
             load_w(0);
             if (!STATES) copy_state();
-            ok = prepare(0);
+            if ((ok = land(0))) {
+                if (!STATES) start_y(0);
+                prepare(0);
+            }
         }
+
         for (int j = 0; j < nc && ok; ++j) {
             const float kappa = ex2_ftz(tot), add = ex2_ftz(tot - ref);
+            const bool was_small = small;
             total += tot;
             if (j + 1 < nc) load_w(j + 1);
-            if (!(ok = wait(ST, j, 168))) break;
+            if (!(ok = wait(ST + (j & 1), j >> 1, 168))) break;
             tc_fence_after();
             const float2 k2 = make_float2(kappa, kappa), a2 = make_float2(add, add);
 #pragma unroll
@@ -662,14 +819,26 @@ __global__ void __launch_bounds__(STATES ? kStThreads : kTcThreads, 1) k_ragged_
                 }
             }
             tc_fence_before();
-            if (j + 1 < nc) {
-                if (!STATES && !(ok = wait(YF, j, 176))) break;   // P X has read w x
-                if (!(ok = prepare(j + 1))) break;
-                if (!STATES) {
-                    if (!(ok = wait(YI, j, 169))) break;   // C S^T has read the copy it is written over
-                    copy_state();
+            if (j + 1 == nc) break;
+            if (!STATES) {
+                if (!(ok = wait(YI, j, 169))) break;   // C S^T has read the copy it is written over
+                copy_state();
+                if (!was_small) {                      // P x of the long form has read x
+                    if (!(ok = wait(YF0 + (j & 1), j >> 1, 178))) break;
+                    if (lane == 0) mbar_arrive(bar(XE));
                 }
+                // the buffer of y is free: the y before last has been read (and the long form's C S^T there)
+                if ((j >= 1 && !(ok = wait(YE0 + ((j - 1) & 1), (j - 1) >> 1, 179))) ||
+                    (!was_small && !(ok = wait(YE0 + (j & 1), j >> 1, 180))))
+                    break;
+                tc_fence_after();
+                if (!(ok = land(j + 1))) break;
+                start_y(j + 1);
+                if (was_small && !(ok = wait(YF0 + (j & 1), j >> 1, 176))) break;   // P X has read w x
+            } else if (!(ok = land(j + 1))) {
+                break;
             }
+            prepare(j + 1);
         }
         if (ok) {
             float *out = nullptr;
@@ -733,16 +902,24 @@ cudaError_t launch_ragged_tc(const RaggedArgs &a, cudaStream_t st) {
     k_ragged_tables<<<dim3(a.seq.tokens / kQ + a.seq.nseq, (a.H + kTabHeads - 1) / kTabHeads), kTabThreads, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = kTcSmem;
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
     if (a.seq.tokens > a.seg) {
         e = cudaFuncSetAttribute(k_ragged_tc<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
         if (e != cudaSuccess) return e;
-        k_ragged_tc<true><<<grid, kStThreads, kTcSmem, st>>>(m, a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = cudaLaunchKernelEx(&cfg, k_ragged_tc<true>, m, a)) != cudaSuccess) return e;
     }
     e = cudaFuncSetAttribute(k_ragged_tc<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
     if (e != cudaSuccess) return e;
-    k_ragged_tc<false><<<grid, kTcThreads, kTcSmem, st>>>(m, a);
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, k_ragged_tc<false>, m, a);
 }
 
 }  // namespace ssd

@@ -847,7 +847,7 @@ ssd_status ragged_plan(const ssd_ragged_shape *s, long long tokens, int nseq, Ra
     if (tokens < 0 || nseq < 0 || tokens + nseq > 0x7fff0000LL) return fail(SSD_ERR_INVALID_ARG, "bad token or sequence count");
     // Tensor-core shapes: one CTA (two heads) to an SM, chunks of 128 tokens; others: about four CTAs to an SM.
     const bool tc = s->io == SSD_BF16 && s->headdim == 64 && s->dstate == 128 && (s->nheads / s->ngroups) % 2 == 0;
-    p->seg = tc ? ssd::ragged_segment(tokens, s->nheads / 2, 128, 2 * 148) : ssd::ragged_segment(tokens, s->nheads, 64, 4 * 148);
+    p->seg = tc ? ssd::ragged_segment(tokens, s->nheads / 2, 128, 2 * 148) : ssd::ragged_segment(tokens, s->nheads, 32, 4 * 148);
     p->units = (int)(tokens / p->seg) + nseq;
     // sequences no longer than a segment need no states between launches
     const size_t n = tokens > p->seg ? (size_t)p->units * s->nheads : 0;

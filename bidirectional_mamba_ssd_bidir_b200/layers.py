@@ -107,7 +107,7 @@ def _f32(name, t, shape, dev):
     """Pointer of a contiguous float32 tensor of this shape (None for None)."""
     if t is None:
         return None
-    if t.dtype is not torch.float32 or t.shape != shape or t.device != dev or not t.is_contiguous():
+    if t.dtype is not torch.float32 or t.shape != shape or t.get_device() != dev.index or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous float32 of shape {tuple(shape)} on {dev}")
     return t.data_ptr()
 
@@ -115,13 +115,27 @@ def _f32(name, t, shape, dev):
 def _i32(name, t, n, dev):
     if t is None:
         return None
-    if t.dtype is not torch.int32 or t.shape != (n,) or t.device != dev or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != (n,) or t.get_device() != dev.index or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 of shape ({n},) on {dev}")
     return t.data_ptr()
 
 
 def _rows(name, t, batched, lead, tail, dtype, dev):
-    """(pointer, elements from one row to the next) of a [tokens, *tail] or [batch, len, *tail] tensor."""
+    """(pointer, elements from one row to the next) of a [tokens, *tail] or [batch, len, *tail] tensor.
+
+    The common case, one token dimension, is told by few tensor calls (a cost of every decoding step); what
+    is not it goes through the checks one by one."""
+    if not batched and t.dtype is dtype and t.shape == lead + tail and t.get_device() == dev.index:
+        st = t.stride()
+        if len(st) == 2:
+            if st[1] == 1 and st[0] >= tail[0]:
+                return t.data_ptr(), st[0]
+        elif st[2] == 1 and st[1] == tail[1] and st[0] >= tail[0] * tail[1]:
+            return t.data_ptr(), st[0]
+    return _rows_checked(name, t, batched, lead, tail, dtype, dev)
+
+
+def _rows_checked(name, t, batched, lead, tail, dtype, dev):
     if t.dtype is not dtype or t.device != dev:
         raise ValueError(f"{name} must be {dtype} on {dev}")
     if t.shape != lead + tail:
@@ -151,24 +165,27 @@ def _width(tail) -> int:
 
 def _packed(x, tail_dims, cu_seqlens, dev):
     """(packed, has a batch dimension, leading shape) of a call whose main tensor is x."""
+    shape = x.shape
     if cu_seqlens is None:
-        if x.dim() != tail_dims + 2:
+        if len(shape) != tail_dims + 2:
             raise ValueError("without cu_seqlens the tensors need a batch and a token dimension")
-        b, n = x.shape[:2]
-        return _Packed(None, b, b * n), True, x.shape[:2]
-    if x.dim() != tail_dims + 1:
+        b, n = shape[:2]
+        return _Packed(None, b, b * n), True, shape[:2]
+    if len(shape) != tail_dims + 1:
         raise ValueError("with cu_seqlens the tensors have one token dimension and no batch dimension")
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+    n = cu_seqlens.numel()
+    if n < 1:
         raise ValueError("cu_seqlens must be int32 of shape (nseq + 1,)")
-    return _Packed(_i32("cu_seqlens", cu_seqlens, cu_seqlens.numel(), dev), cu_seqlens.numel() - 1, x.shape[0]), False, x.shape[:1]
+    return _Packed(_i32("cu_seqlens", cu_seqlens, n, dev), n - 1, shape[0]), False, shape[:1]
 
 
 def _pool(name, t, tail, dtype, dev):
     if t is None:
         return None, 0
-    if t.dtype is not dtype or t.device != dev or t.shape[1:] != tail or t.dim() != len(tail) + 1 or not t.is_contiguous():
+    shape = t.shape
+    if t.dtype is not dtype or shape[1:] != tail or len(shape) != len(tail) + 1 or t.get_device() != dev.index or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} of shape (slots, {', '.join(map(str, tail))}) on {dev}")
-    return t.data_ptr(), t.shape[0]
+    return t.data_ptr(), shape[0]
 
 
 def _slots(state_in, state_out, slots_in, slots_out, tail, dtype, nseq, dev):
@@ -182,11 +199,25 @@ def _slots(state_in, state_out, slots_in, slots_out, tail, dtype, nseq, dev):
                                n_in, n_out))
 
 
-def _scratch(workspace, need, dev):
-    """(tensor, pointer, bytes) of the caller's workspace, or of one taken here."""
+_need: dict = {}
+
+
+def _bytes(f, *key) -> int:
+    """Workspace size f(*key) (a pure function of the shape), asked for once per shape."""
+    n = _need.get(key)
+    if n is None:
+        if len(_need) > 4096:
+            _need.clear()
+        n = _need[key] = max(256, int(f(*key[1:])))
+    return n
+
+
+def _scratch(workspace, need, like):
+    """(tensor, pointer, bytes) of the caller's workspace, or of one taken here on ``like``'s device."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = like.new_empty(need, dtype=torch.uint8)
         return workspace, workspace.data_ptr(), need
+    dev = like.device
     if workspace.device != dev or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
     return workspace, workspace.data_ptr(), workspace.numel()
@@ -207,6 +238,18 @@ def _no_overlap(out, yp, ldy, width, rows, *ins):
         raise ValueError("out overlaps an input")
 
 
+def _conv_bwd_bytes(C, K, tokens):
+    return lib.ssd_conv_bwd_workspace_bytes(_ConvShape(C, K, 1, 1, 0), tokens)
+
+
+def _ragged_bytes(H, P, N, G, io, tokens, nseq):
+    return lib.ssd_ragged_workspace_bytes(_RaggedShape(H, P, N, G, io), tokens, nseq)
+
+
+def _step_bytes(R, H, P, N, G, K):
+    return lib.ssd_step_workspace_bytes(_StepShape(R, R, H, P, N, G, K, 0))
+
+
 def ssd_conv(x, w, bias=None, cu_seqlens=None, direction: int = 1, silu: bool = True, state_in=None, state_out=None,
              slots_in=None, slots_out=None, out=None, workspace=None):
     """The depthwise causal convolution (then SiLU): returns y shaped like x.
@@ -222,12 +265,12 @@ def ssd_conv(x, w, bias=None, cu_seqlens=None, direction: int = 1, silu: bool = 
     C, K = w.shape
     seq, batched, lead = _packed(x, 1, cu_seqlens, dev)
     xp, ldx = _rows("x", x, batched, lead, (C,), x.dtype, dev)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
-    yp, ldy = _rows("out", y, batched, lead, (C,), x.dtype, dev)
+    y = x.new_empty(x.shape) if out is None else out
+    yp, ldy = (y.data_ptr(), C) if out is None else _rows("out", y, batched, lead, (C,), x.dtype, dev)
     if out is not None:
         _no_overlap(out, yp, ldy, C, seq.tokens, (x, xp, ldx, C))
     slots = _slots(state_in, state_out, slots_in, slots_out, (K - 1, C), x.dtype, seq.nseq, dev)
-    ws, wp, wn = (None, None, 0) if workspace is None else _scratch(workspace, 256, dev)
+    ws, wp, wn = (None, None, 0) if workspace is None else _scratch(workspace, 256, x)
     _call(dev, lib.ssd_conv, _ConvShape(C, K, int(direction), int(silu), io), seq, xp, ldx, _f32("w", w, (C, K), dev),
           _f32("bias", bias, (C,), dev), slots, yp, ldy, wp, wn)
     return y
@@ -243,11 +286,11 @@ def ssd_conv_bwd(x, w, bias, gy, cu_seqlens=None, direction: int = 1, silu: bool
     seq, batched, lead = _packed(x, 1, cu_seqlens, dev)
     xp, ldx = _rows("x", x, batched, lead, (C,), x.dtype, dev)
     gp, ldg = _rows("gy", gy, batched, lead, (C,), x.dtype, dev)
-    gx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    gw = torch.empty((C, K), dtype=torch.float32, device=dev)
-    gb = torch.empty((C,), dtype=torch.float32, device=dev) if bias is not None else None
+    gx = x.new_empty(x.shape)
+    gw = torch.empty_like(w, memory_format=torch.contiguous_format)
+    gb = torch.empty_like(bias, memory_format=torch.contiguous_format) if bias is not None else None
     shape = _ConvShape(C, K, int(direction), int(silu), io)
-    ws, wp, wn = _scratch(workspace, max(256, lib.ssd_conv_bwd_workspace_bytes(shape, seq.tokens)), dev)
+    ws, wp, wn = _scratch(workspace, _bytes(_conv_bwd_bytes, "conv", C, K, seq.tokens), x)
     _call(dev, lib.ssd_conv_bwd, shape, seq, xp, ldx, _f32("w", w, (C, K), dev), _f32("bias", bias, (C,), dev), gp, ldg,
           gx.data_ptr(), C, gw.data_ptr(), gb.data_ptr() if gb is not None else None, wp, wn)
     return {"x": gx, "w": gw, "bias": gb}
@@ -277,8 +320,8 @@ def ssd_scan_ragged(x, dt, A, B, C, D=None, cu_seqlens=None, dt_bias=None, direc
     dp, ldd = _rows("dt", dt, batched, lead, (H,), x.dtype, dev)
     bp, ldb = _rows("B", B, batched, lead, (G, N), x.dtype, dev)
     cp, ldc = _rows("C", C, batched, lead, (G, N), x.dtype, dev)
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
-    yp, ldy = _rows("out", y, batched, lead, (H, P), x.dtype, dev)
+    y = x.new_empty(x.shape) if out is None else out
+    yp, ldy = (y.data_ptr(), H * P) if out is None else _rows("out", y, batched, lead, (H, P), x.dtype, dev)
     if out is not None:
         _no_overlap(out, yp, ldy, H * P, seq.tokens, (x, xp, ldx, H * P), (dt, dp, ldd, H), (B, bp, ldb, G * N),
                     (C, cp, ldc, G * N))
@@ -286,7 +329,7 @@ def ssd_scan_ragged(x, dt, A, B, C, D=None, cu_seqlens=None, dt_bias=None, direc
     shape = _RaggedShape(H, P, N, G, io)
     prm = _RaggedParams(xp, dp, bp, cp, ldx, ldd, ldb, ldc, _f32("A", A, (H,), dev), _f32("D", D, (H,), dev),
                         _f32("dt_bias", dt_bias, (H,), dev))
-    ws, wp, wn = _scratch(workspace, max(256, lib.ssd_ragged_workspace_bytes(shape, seq.tokens, seq.nseq)), dev)
+    ws, wp, wn = _scratch(workspace, _bytes(_ragged_bytes, "ragged", H, P, N, G, io, seq.tokens, seq.nseq), x)
     _call(dev, lib.ssd_scan_ragged, shape, seq, prm, int(direction), slots, yp, ldy, wp, wn)
     return y
 
@@ -320,12 +363,12 @@ def mamba2_step(xBC, dt, conv_w, conv_b, dt_bias, A, D, conv_state, ssm_state, s
     vp, nc = _pool("conv_state", conv_state, (K - 1, Cc), dtype, dev)
     if nc != n:
         raise ValueError(f"conv_state has {nc} slots, ssm_state {n}")
-    y = torch.empty((R, H, P), dtype=dtype, device=dev) if out is None else out
-    yp, ldy = _rows("out", y, False, lead, (H, P), dtype, dev)
+    y = xBC.new_empty((R, H, P)) if out is None else out
+    yp, ldy = (y.data_ptr(), H * P) if out is None else _rows("out", y, False, lead, (H, P), dtype, dev)
     if out is not None:
         _no_overlap(out, yp, ldy, H * P, R, (xBC, xp, ldx, Cc), (dt, dp, ldd, H))
     shape = _StepShape(R, n, H, P, N, ngroups, K, io)
-    ws, wp, wn = _scratch(workspace, max(256, lib.ssd_step_workspace_bytes(shape)), dev)
+    ws, wp, wn = _scratch(workspace, _bytes(_step_bytes, "step", R, H, P, N, ngroups, K), xBC)
     _call(dev, lib.mamba2_step, shape, xp, ldx, dp, ldd, _f32("conv_w", conv_w, (Cc, K), dev), _f32("conv_b", conv_b, (Cc,), dev),
           _f32("dt_bias", dt_bias, (H,), dev), _f32("A", A, (H,), dev), _f32("D", D, (H,), dev), vp, sp,
           _i32("slots", slots, R, dev), yp, ldy, wp, wn)
@@ -345,7 +388,7 @@ def _ffn_shape(u, W_in, W_out, activation, dev):
 
 
 def _bf16(name, t, shape, dev):
-    if t.dtype is not torch.bfloat16 or t.shape != shape or t.device != dev or not t.is_contiguous():
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev.index or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous bf16 of shape {tuple(shape)} on {dev}")
     return t.data_ptr()
 
@@ -369,14 +412,14 @@ def ffn_block(u, W_in, W_out, activation: str = "silu", save: bool = False, out=
     shape = _ffn_shape(u, W_in, W_out, activation, dev)
     D, F, lead = shape.d_model, shape.d_ff, u.shape[:-1]
     up, wi, wo = _bf16("u", u, lead + (D,), dev), _bf16("W_in", W_in, (2 * F, D), dev), _bf16("W_out", W_out, (D, F), dev)
-    y = torch.empty(u.shape, dtype=torch.bfloat16, device=dev) if out is None else out
-    yp = _bf16("out", y, lead + (D,), dev)
+    y = u.new_empty(u.shape) if out is None else out
+    yp = y.data_ptr() if out is None else _bf16("out", y, lead + (D,), dev)
     if out is not None:
         for name, t in (("u", u), ("W_in", W_in), ("W_out", W_out)):
             if yp < t.data_ptr() + 2 * t.numel() and t.data_ptr() < yp + 2 * y.numel():
                 raise ValueError(f"out overlaps {name}")
-    gu = torch.empty(lead + (2 * F,), dtype=torch.bfloat16, device=dev) if save else None
-    ws, wp, wn = _scratch(workspace, max(256, lib.ssd_ffn_workspace_bytes(shape)), dev)
+    gu = u.new_empty(lead + (2 * F,)) if save else None
+    ws, wp, wn = _scratch(workspace, _bytes(ffn_workspace_bytes, "ffn", shape.tokens, D, F), u)
     _call(dev, lib.ffn_block, shape, up, wi, wo, yp, gu.data_ptr() if save else None, wp, wn)
     return (y, gu) if save else y
 
@@ -389,6 +432,6 @@ def ffn_block_bwd(u, W_in, W_out, gu, gy, activation: str = "silu", workspace=No
     ptrs = [_bf16("u", u, lead + (D,), dev), _bf16("W_in", W_in, (2 * F, D), dev), _bf16("W_out", W_out, (D, F), dev),
             _bf16("gu", gu, lead + (2 * F,), dev), _bf16("gy", gy, lead + (D,), dev)]
     g = {"u": torch.empty_like(u), "W_in": torch.empty_like(W_in), "W_out": torch.empty_like(W_out)}
-    ws, wp, wn = _scratch(workspace, max(256, lib.ssd_ffn_bwd_workspace_bytes(shape)), dev)
+    ws, wp, wn = _scratch(workspace, _bytes(ffn_bwd_workspace_bytes, "ffn bwd", shape.tokens, D, F), u)
     _call(dev, lib.ffn_block_bwd, shape, *ptrs, g["u"].data_ptr(), g["W_in"].data_ptr(), g["W_out"].data_ptr(), wp, wn)
     return g

@@ -1,4 +1,4 @@
-"""Float64 forms of the layer operators on packed ragged batches (torch on the CPU, one sequence at a time).
+"""Float64 forms of the layer operators on packed ragged batches (torch, one sequence at a time, on the inputs' device).
 
 Every function also returns what a tolerance needs: the same sums over absolute values.  Nothing here
 is shared with the CUDA path.
@@ -74,12 +74,12 @@ def scan(x, dt, A, B, C, D, lens, dt_bias=None, direction=1, start=None):
     G, N = B.shape[1:]
     if dt_bias is not None:
         dt = softplus(dt + dt_bias.double())
-    d = D.double() if D is not None else torch.zeros(H, dtype=torch.float64)
+    d = D.double() if D is not None else torch.zeros(H, dtype=torch.float64, device=x.device)
     Bh, Ch = B.repeat_interleave(H // G, 1), C.repeat_interleave(H // G, 1)
     y, ym, last, lastm = torch.zeros_like(x), torch.zeros_like(x), [], []
     lo = 0
     for i, n in enumerate(lens):
-        S = start[i].double().clone() if start is not None and start[i] is not None else torch.zeros(H, P, N, dtype=torch.float64)
+        S = start[i].double().clone() if start is not None and start[i] is not None else torch.zeros(H, P, N, dtype=torch.float64, device=x.device)
         M = S.abs()
         for t in _order(n, direction):
             t += lo

@@ -267,6 +267,34 @@ def test_scan_ragged_tensor_core_steep_and_flat(ssd, direction):
     _scan_case(ssd, [300, 77], 4, 64, 128, 1, "bf16", direction, False, True, _tc_y, _tc_s, A=A)
 
 
+# Several chunks to a segment, several segments to a sequence, with states kept between them: enough heads and
+# tokens that a segment is 2 to 7 chunks of 128 (the more heads, the longer the segments).
+LONG = [([3000], 64, 1, 1, True), ([1500, 700, 811], 64, 1, -1, False), ([2600, 1, 399], 64, 2, 1, True), ([7003], 64, 4, 1, False),
+        ([2304, 2304], 32, 1, -1, True)]
+
+
+@pytest.mark.parametrize("steep", [1.0, 8.0], ids=["flat", "steep"])
+@pytest.mark.parametrize("lens,H,G,direction,carry", LONG, ids=str)
+def test_scan_ragged_tensor_core_long(ssd, lens, H, G, direction, carry, steep):
+    """As above on long sequences, float64 on the GPU; `steep` sends part of the heads through the long form
+    (alternating with the short one from chunk to chunk)."""
+    P, N, T, S = 64, 128, sum(lens), len(lens)
+    g = _gen(tuple(lens), H, steep)
+    _, x, B, C, d, A, D, _ = _scan_inputs(g, T, H, P, N, G, torch.bfloat16, False)
+    # stretches of larger steps, so that the chunks of one head differ
+    d = (d.float() * (1 + (steep - 1) * (torch.arange(T) // 300 % 3 == 1).float()[:, None])).to(torch.bfloat16)
+    x, B, C, d, A, D = (v.contiguous().cuda() for v in (x, B, C, d, A, D))
+    pool = torch.randn(S, H, P, N, generator=g).cuda()
+    start = [pool[i].clone() for i in range(S)] if carry else None
+    ws = torch.zeros(ssd.ragged_workspace_bytes(T, S, H, P, N, G), dtype=torch.uint8, device="cuda")
+    y = ssd.ssd_scan_ragged(x, d, A, B, C, D, cu_seqlens=_cu(lens), direction=direction, state_in=pool if carry else None,
+                            state_out=pool, workspace=ws)
+    ssd.workspace_status(ws)
+    ref, ym, last, lastm = ol.scan(x, d, A, B, C, D, lens, None, direction, start)
+    _check(y, ref.cpu(), _tc_y(max(lens), N, ref.cpu(), ym.cpu()), "y")
+    for i in range(S):
+        _check(pool[i], last[i].cpu(), _tc_s(lens[i], last[i].cpu(), lastm[i].cpu()), f"state {i}")
+
 def test_scan_ragged_neighbours_do_not_leak(ssd):
     """NaN and infinity in one sequence (and behind the last) leave the others bit for bit, states too."""
     g = _gen("leak")
