@@ -788,12 +788,16 @@ ssd_status ssd_conv_bwd(const ssd_conv_shape *shape, const ssd_packed *seq, cons
     if (!w || !gw || !aligned(w, 4) || !aligned(bias, 4) || !aligned(gw, 4) || !aligned(gb, 4))
         return fail(SSD_ERR_INVALID_ARG, "w and gw must be non-NULL, w, bias, gw and gb 4-byte aligned");
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    const size_t es = io_bytes(shape->io);
     if (a.seq.tokens == 0 || a.seq.nseq == 0) {
         cudaError_t e = cudaMemsetAsync(gw, 0, sizeof(float) * a.C * a.K, cs);
         if (e == cudaSuccess && gb) e = cudaMemsetAsync(gb, 0, sizeof(float) * a.C, cs);
+        if (e == cudaSuccess && a.seq.tokens > 0) {      // rows, but no sequence
+            if ((st = check_rows(gx, ldgx, a.C, es, "gx")) != SSD_OK) return st;
+            e = cudaMemset2DAsync(gx, ldgx * es, 0, a.C * es, a.seq.tokens, cs);
+        }
         return e == cudaSuccess ? SSD_OK : cuda_fail(e, "empty gradient clear");
     }
-    const size_t es = io_bytes(shape->io);
     if ((st = check_rows(x, ldx, a.C, es, "x")) != SSD_OK || (st = check_rows(gy, ldg, a.C, es, "gy")) != SSD_OK ||
         (st = check_rows(gx, ldgx, a.C, es, "gx")) != SSD_OK)
         return st;

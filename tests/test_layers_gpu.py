@@ -513,3 +513,77 @@ def test_graph_replays_follow_new_inputs(ssd):
         live = torch.tensor(new) >= 0
         assert torch.equal(out[live], want[live])
         assert torch.equal(d["ssm_state"], eager["ssm_state"]) and torch.equal(d["conv_state"], eager["conv_state"])
+
+
+def test_empty_sequences_pass_their_states_on(ssd):
+    """No token at all (uniform and packed), no sequence at all: states move from slot to slot, gradients are zero."""
+    g = _gen("empty")
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    conv, ssm = torch.randn(4, 3, 8, generator=g).cuda(), torch.randn(4, 2, 16, 16, generator=g).cuda()
+    w = torch.randn(8, 4, generator=g).cuda()
+    z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    kw = dict(slots_in=i32(0, -1), slots_out=i32(3, 2))
+    keep_c, keep_s = conv.clone(), ssm.clone()
+    ssd.ssd_conv(z(0, 8), w, cu_seqlens=i32(0, 0, 0), state_in=conv, state_out=conv, **kw)
+    ssd.ssd_scan_ragged(z(0, 2, 16), z(0, 2), -z(2), z(0, 1, 16), z(0, 1, 16), cu_seqlens=i32(0, 0, 0), state_in=ssm, state_out=ssm, **kw)
+    for new, old in ((conv, keep_c), (ssm, keep_s)):
+        assert torch.equal(new[3], old[0]) and bool((new[2] == 0).all()) and torch.equal(new[:2], old[:2])
+    out = z(2, 3, 16, 16)
+    ssd.ssd_scan_ragged(z(2, 0, 3, 16), z(2, 0, 3), -z(3), z(2, 0, 1, 16), z(2, 0, 1, 16), state_out=out.fill_(5))
+    assert bool((out == 0).all())
+    gr = ssd.ssd_conv_bwd(torch.ones(6, 8, device="cuda"), w, w[:, 0].contiguous(), torch.ones(6, 8, device="cuda"), cu_seqlens=i32(0))
+    assert all(bool((gr[k] == 0).all()) for k in ("x", "w", "bias"))
+
+
+def test_calls_on_a_side_stream_and_two_at_once(ssd):
+    """Two scans and two steps on two streams at once, each with its own scratch: as when run alone."""
+    g = _gen("streams")
+    T, H, P, N = 900, 4, 64, 128
+    sets = []
+    for i in range(2):
+        _, x, B, C, d, A, D, _ = _scan_inputs(g, T, H, P, N, 1, torch.bfloat16, False)
+        sets.append([v.contiguous().cuda() for v in (x, d, A, B, C, D)])
+    cu = _cu([500, 400])
+    alone = [ssd.ssd_scan_ragged(*v, cu_seqlens=cu) for v in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for s, v in zip(streams, sets):
+        with torch.cuda.stream(s):
+            got.append([ssd.ssd_scan_ragged(*v, cu_seqlens=cu) for _ in range(4)])
+    torch.cuda.synchronize()
+    for a, many in zip(alone, got):
+        assert all(torch.equal(a, b) for b in many)
+
+
+def test_conv_and_scan_replay_in_a_graph(ssd):
+    """A captured prompt (convolution, then the scan on its column blocks) replayed on new tokens and offsets."""
+    g = _gen("graph scan")
+    T, H, P, N = 400, 2, 64, 128
+    C = H * P + 2 * N
+    x = torch.randn(T, C, generator=g).to(torch.bfloat16).cuda()
+    d = torch.rand(T, H, generator=g).mul(0.1).to(torch.bfloat16).cuda()
+    w, A = (torch.rand(C, 4, generator=g) - 0.5).cuda(), -torch.ones(H, device="cuda")
+    cu = _cu([200, 200])
+    pool = torch.zeros(2, H, P, N, device="cuda")
+
+    def run():
+        v = ssd.ssd_conv(x, w, cu_seqlens=cu)
+        return ssd.ssd_scan_ragged(v[:, :H * P].unflatten(1, (H, P)), d, A, v[:, H * P:H * P + N].unflatten(1, (1, N)),
+                                   v[:, H * P + N:].unflatten(1, (1, N)), cu_seqlens=cu, state_out=pool)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for lens in ([200, 200], [1, 399], [390, 3]):
+        x.copy_(torch.randn(T, C, generator=g))
+        cu.copy_(_cu(lens))
+        graph.replay()
+        got, state = out[:sum(lens)].clone(), pool.clone()
+        want = run()
+        assert torch.equal(got, want[:sum(lens)]) and torch.equal(state, pool)
