@@ -10,16 +10,16 @@
 //   y_i       = rho_i (scores (w x) + C (exp(m) S)^T)_i + D x_i
 //   S        <- exp(c) S + exp(c - m) sum_j (w_j x_j) (outer) B_j
 //
-// With m = c / 2 the exponents of w and rho stay within half the chunk's decay: no factor of the decay
+// With m about c / 2 the exponents of w and rho stay within half the chunk's decay: no factor of the decay
 // touches an element of the scores, which are rounded to bf16 as they are and serve both heads.  A
 // chunk that decays by more than 2^150 for one of the two heads takes the long form for both: m = c
 // (no exponent of w is positive), P = scores times the decay, formed for each head, and x as it is in
 // the place of w x.
 //
 // Precision.  The scores (or P), w x in their product and the copy of S that multiplies C are rounded
-// to bf16 (operands of products whose result is a bf16 y).  S itself is a float32 output, so w x
-// enters its product in two bf16 terms, high and rest: 2^-17 of w x instead of 2^-9.  S stays in
-// registers in float32.
+// to bf16 (operands of products whose result is a bf16 y).  S itself is a float32 output: w x enters its
+// product in three bf16 terms, each the bf16 of what the ones before leave (2^-25 of w x in all; two
+// terms, 2^-17, gave states 2e-6 off, twenty times float32's error), and S stays in registers in float32.
 //
 // Products (M = 128 each, float32 in TMEM):
 //   scores    [0,128)    A = C, B = B tile, both K-major in smem
@@ -27,7 +27,7 @@
 //                        A = C, B = bf16 exp(m) S of both heads (MN-major: row n, 128 columns (head, p));
 //                        then A = P (bf16, in TMEM over the scores: 32 columns of scores become 16 of P),
 //                        B = high of w x (MN-major), N = 128.  y = rho (the sum).
-//   new S     [128,256)  A = B^T (MN-major, M = n), B = w x high, then rest (MN-major), N = 128
+//   new S     [128,256)  A = B^T (MN-major, M = n), B = the terms of w x one after the other (MN-major), N = 128
 // In the long form C S^T, with S as it is, goes to the other buffer of y, 16 columns of each head's P
 // take the place of 32 of scores, and P x is formed a head at a time, N = 64.
 //
@@ -72,13 +72,13 @@ constexpr int kGroup = 8;                              // warps of a group
 
 // shared memory: everything but the tables in 16 KB boxes; 227 KB in all
 constexpr uint32_t kSX = 0;                            // x of two heads (STATES: a second stage where C is otherwise)
-constexpr uint32_t kSW = 4 * kBox;                     // w x: high of two heads, rest of two heads
-constexpr uint32_t kSB = 8 * kBox, kSB1 = 2 * kBox, kSC = 10 * kBox;   // B (two stages), C: two 64-column boxes each
+constexpr uint32_t kSW = 2 * kBox;                     // w x: three terms of two heads each
+constexpr uint32_t kSB = 8 * kBox, kSC = 10 * kBox;    // B, C: two 64-column boxes each
 constexpr uint32_t kSS = 12 * kBox;                    // bf16 S: rows n, a box per head
 // One chunk and head's table: the column factors, which every warp reads (copied to shared memory):
 // q of the diagonal blocks, then of row blocks 1, 2, 3 (32, 64 and 96 columns); cs_b of the row blocks,
 // the chunk's decay, the steep blocks' bits,
-// m, and whether the pair takes the short form.  Then per-row values.
+// m, and 0 in the long form or 1 + m - c.  Then per-row values.
 constexpr int kTabQd = 0, kTabQ = 128, kTabRef = 320, kTabTot = 324, kTabSteep = 325, kTabM = 326, kTabShort = 327, kTabShared = 328;
 constexpr int kTabRho = 328, kTabW = 456, kTabCs = 584, kTabCsd = 712, kTabLen = 840;   // kTabRho: log2 rho
 constexpr float kSteepBlock = 60.f, kSteepChunk = 150.f;
@@ -157,7 +157,9 @@ __global__ void __launch_bounds__(kTabThreads) k_ragged_tables(const __grid_cons
         if (g0 + i >= a.H) return;
         // (H is even, and the pairs begin at even heads)
         const bool small = -tots[i] <= kSteepChunk && -tots[i ^ 1] <= kSteepChunk;
-        const float m = small ? 0.5f * tot : tot;
+        // m - c is a whole number of powers of two, so that exp(c - m) is exact and w keeps the accuracy of
+        // the sum behind its token
+        const float up2 = small ? rintf(-0.5f * tot) : 0.f, m = tot + up2;
         float *out = a.tables + ((size_t)c * a.H + g0 + i) * kTabLen;
         float cs[4];
 #pragma unroll
@@ -174,8 +176,7 @@ __global__ void __launch_bounds__(kTabThreads) k_ragged_tables(const __grid_cons
         for (int e = 0; e < 4; ++e) {
             const int k = 4 * lane + e, row = a.dir > 0 ? k : kQ - 1 - k;      // row of the tile
             out[kTabRho + row] = small ? cs[e] - m : steep_own ? 0.f : cs[e] - own;
-            // (the long form's exponent is the sum itself, not a difference)
-            out[kTabW + row] = dt[e] * ex2_ftz(small ? m - cs[e] : ed + dn[e]);
+            out[kTabW + row] = dt[e] * ex2_ftz(ed + dn[e] + up2);
             if (small) continue;                       // the rest is the long form's
             out[kTabCs + row] = cs[e];
             out[kTabCsd + row] = cs[e] - __log2f(dt[e]);
@@ -193,7 +194,7 @@ __global__ void __launch_bounds__(kTabThreads) k_ragged_tables(const __grid_cons
             }
             out[kTabTot] = tot;
             out[kTabM] = m;
-            out[kTabShort] = small ? 1.f : 0.f;
+            out[kTabShort] = small ? up2 + 1.f : 0.f;
             out[kTabSteep] = __int_as_float(steep);
         }
     }
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
     const uint32_t tmem = *tmem_slot;
     auto wait = [&](int b, int phase, int code) { return mbar_wait(bar(b), (uint32_t)phase & 1, MASK, abort_flag, a.status, code); };
 
-    // w x of chunk j in two bf16 terms: this thread's row, 32 of the head's columns; rows of no token zero
+    // w x of chunk j in three bf16 terms: this thread's row, 32 of the head's columns; rows of no token zero
     auto weigh = [&](int j, int row, int hh, int side, float w) {
         const int n = rows(j);
         const bool mine = a.dir > 0 ? row < n : row >= kQ - n;
@@ -285,16 +286,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
             uint4 v = *reinterpret_cast<const uint4 *>(x + off);
             if (!mine) v = make_uint4(0u, 0u, 0u, 0u);
             const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-            uint32_t hi[4], lo[4];
+            uint32_t t[3][4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 f = mul2(unpack2(in[e]), w2);
-                hi[e] = pack_bf16(f.x, f.y);
-                const float2 rest = fma2(unpack2(hi[e]), m1, f);
-                lo[e] = pack_bf16(rest.x, rest.y);
+                float2 f = mul2(unpack2(in[e]), w2);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    t[k][e] = pack_bf16(f.x, f.y);
+                    if (k < 2) f = fma2(unpack2(t[k][e]), m1, f);   // exact
+                }
             }
-            *reinterpret_cast<uint4 *>(to + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4 *>(to + 2 * kBox + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+            for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4 *>(to + 2 * k * kBox + off) = make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
         }
         fence_async_smem();
         __syncwarp();
@@ -332,10 +335,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
                 mbar_expect_tx(bar(XF + st), 2 * kBox);
                 for (int h = 0; h < 2; ++h) tma_load_2d(sbase + (st ? kSC : kSX) + h * kBox, &maps.x, 64 * (h0 + h), r, bar(XF + st));
                 nx = j + 1;
-                if (j >= 2 && !wait1(BE + (j & 1), (j >> 1) - 1, 152)) break;
+                if (j >= 1 && !wait1(BE + ((j - 1) & 1), (j - 1) >> 1, 152)) break;
                 mbar_expect_tx(bar(BF + (j & 1)), 2 * kBox);
                 for (int h = 0; h < 2; ++h)
-                    tma_load_2d(sbase + (j & 1 ? kSB1 : kSB) + h * kBox, &maps.b, 128 * grp + 64 * h, r, bar(BF + (j & 1)));
+                    tma_load_2d(sbase + kSB + h * kBox, &maps.b, 128 * grp + 64 * h, r, bar(BF + (j & 1)));
                 nb = j + 1;
                 if (STATES) continue;
                 if (j >= 1 && !wait1(CE, j - 1, 153)) break;
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
             if (*abort_flag) {                         // copies in flight land before the memory is given up
                 for (int j = nx - 1; j >= 0 && j >= nx - (STATES ? 2 : 1); --j)
                     mbar_drain(bar(XF + (STATES ? j & 1 : 0)), (uint32_t)(STATES ? j >> 1 : j) & 1, a.wait_cycles);
-                for (int j = nb - 1; j >= 0 && j >= nb - 2; --j) mbar_drain(bar(BF + (j & 1)), (uint32_t)(j >> 1) & 1, a.wait_cycles);
+                if (nb) mbar_drain(bar(BF + ((nb - 1) & 1)), (uint32_t)((nb - 1) >> 1) & 1, a.wait_cycles);
                 if (ncc) mbar_drain(bar(CF), (uint32_t)(ncc - 1) & 1, a.wait_cycles);
                 if (nt) mbar_drain(bar(TF), (uint32_t)(nt - 1) & 1, a.wait_cycles);
             }
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
         // ------------------------------------------------------------ products that read C: scores, C S^T
         if (!STATES) {
             const uint32_t id_sc = idesc(128, 0, 0), id_yi = idesc(128, 0, 1);
-            const SDesc dC = make_sdesc(sbase + kSC, 16, 1024), dB0 = make_sdesc(sbase + kSB, 16, 1024), dB1 = make_sdesc(sbase + kSB1, 16, 1024), dS = make_sdesc(sbase + kSS, kBox, 1024);
+            const SDesc dC = make_sdesc(sbase + kSC, 16, 1024), dBk = make_sdesc(sbase + kSB, 16, 1024), dS = make_sdesc(sbase + kSS, kBox, 1024);
             const float *tg = a.tables + ((size_t)chunk0 * a.H + h0) * kTabLen + kTabShort;
             float next = nc > 0 ? *tg : 0.f;
             for (int j = 0; j < nc; ++j) {
@@ -381,7 +384,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
                 if (j + 1 < nc) next = *tg;
                 // P of the chunk before lies over the scores until its product has read it; a partial
                 // chunk's B is zeroed in part first
-                const SDesc dBk = j & 1 ? dB1 : dB0;
                 if (!wait(BF + (j & 1), j >> 1, 155) || !wait(CF, j, 157) || (j >= 1 && !wait(YF0 + ((j - 1) & 1), (j - 1) >> 1, 156)) ||
                     (rows(j) < kQ && !wait(PREP + (j & 1), j >> 1, 154)))
                     break;
@@ -416,14 +418,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
     } else if (warp == 18) {
         // ------------------------------------------------------------ the product of the state (K = tokens: 16 rows of 128 bytes to a step)
         const uint32_t id_st = idesc(128, 1, 1);
-        const SDesc dB0 = make_sdesc(sbase + kSB, kBox, 1024), dB1 = make_sdesc(sbase + kSB1, kBox, 1024), dW = make_sdesc(sbase + kSW, kBox, 1024);
+        const SDesc dBm = make_sdesc(sbase + kSB, kBox, 1024), dW = make_sdesc(sbase + kSW, kBox, 1024);
         for (int j = 0; j < nc; ++j) {
-            const SDesc dBm = j & 1 ? dB1 : dB0;
             if (!wait(PREP + (j & 1), j >> 1, 160) || !wait(BF + (j & 1), j >> 1, 172)) break;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < 16; ++ks)
+                for (int ks = 0; ks < 24; ++ks)
                     mma_ss(tmem + kColS, dBm.at((ks & 7) * 2048), dW.at((ks >> 3) * 2 * kBox + (ks & 7) * 2048), id_st, ks > 0);
                 mma_commit(bar(ST + (j & 1)));
                 mma_commit(bar(BE + (j & 1)));
@@ -711,6 +712,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
         }
         // Of the chunk that is next: w and log2 rho of this row, c and m (log2), its form
         float wr = 0.f, lr = 0.f, tot = 0.f, ref = 0.f, total = 0.f;
+        float shortness = 0.f;                         // kTabShort
         bool small = false;
         const float Dh = a.D ? a.D[h] : 0.f;
         auto load_w = [&](int j) {
@@ -719,7 +721,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
             lr = t[kTabRho + row];
             tot = t[kTabTot];
             ref = t[kTabM];
-            small = t[kTabShort] != 0.f;
+            shortness = t[kTabShort];
+            small = shortness != 0.f;
         };
         auto copy_state = [&]() {                      // bf16 exp(m) S (long form: S): row n of the head's box
             const float f = small ? ex2_ftz(ref) : 1.f;
@@ -750,7 +753,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         if (!STATES) *reinterpret_cast<uint4 *>(xb + swz(row, i)) = make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4 *>(sm + (j & 1 ? kSB1 : kSB) + hh * kBox + swz(row, i)) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(sm + kSB + hh * kBox + swz(row, i)) = make_uint4(0u, 0u, 0u, 0u);
                     }
             }
             return true;
@@ -800,7 +803,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
         }
 
         for (int j = 0; j < nc && ok; ++j) {
-            const float kappa = ex2_ftz(tot), add = ex2_ftz(tot - ref);
+            const float kappa = ex2_ftz(tot), add = small ? ex2_ftz(1.f - shortness) : 1.f;
             const bool was_small = small;
             total += tot;
             if (j + 1 < nc) load_w(j + 1);

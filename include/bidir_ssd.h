@@ -415,8 +415,8 @@ ssd_status ssd_conv_bwd(const ssd_conv_shape *shape, const ssd_packed *seq, cons
  * bf16 with headdim 64, dstate 128, an even number of heads to a group and rows
  * that are multiples of 16 bytes runs on the tensor cores in chunks of 128
  * tokens: scores, inputs and the copy of the state that meets C are rounded to
- * bf16 there, the state itself is float32 from products of two bf16 terms
- * (2^-17).  A NaN or an infinity in x, B, C or dt may reach the up to 127 tokens
+ * bf16 there; the state itself is float32, from products of three bf16 terms
+ * (2^-25).  A NaN or an infinity in x, B, C or dt may reach the up to 127 tokens
  * before its own in the same sequence; it never reaches another sequence. */
 typedef struct {
     int nheads, headdim, dstate, ngroups;

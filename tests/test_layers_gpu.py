@@ -237,8 +237,9 @@ def test_scan_ragged_pieces_equal_the_whole(ssd):
 # S is rounded to bf16 where it meets C (2^-8); y is rounded (2^-8).  With Y the recurrence over
 # absolute values: |dy| <= 2^-8 |y| + (1 + 2^-8) (2 2^-8 + 2^-16 + 2^-12) Y, 2^-12 being room for exponents (|cs|
 # up to 500: 500 u ln 2 times a few) and float32 sums.
-# The state: w x in two bf16 terms is within 2^-17 (a half step of 2^-9 of a rest of at most 2^-8), B exact;
-# w is within (|cs| + 8) 2 u, sums and decays of n / 128 chunks some 3 u each: (2^-17 + 2^-14) S.
+# The state: w x in three bf16 terms is within 2^-24 (each term leaves at most half a step, 2^-8, of what
+# it stands for), B exact; w is within (|cs| + 8) 2 u, |cs| up to 500, sums and decays of n / 128 chunks
+# some 3 u each: 2^-14 S.
 TC = [
     ([1], 2, 1, 1), ([128], 2, 1, 1), ([127, 129], 4, 2, -1), ([5, 0, 300, 64], 4, 1, 1), ([5, 0, 300, 64], 4, 1, -1),
     ([700], 2, 1, 1), ([513, 130], 2, 1, -1), ([256, 384], 8, 4, 1), ([1] * 9, 2, 1, 1),
@@ -250,7 +251,7 @@ def _tc_y(n, N, y, ym):
 
 
 def _tc_s(n, s, sm):
-    return (2.0 ** -17 + 2.0 ** -14) * sm + 1e-37
+    return 2.0 ** -14 * sm + 1e-37
 
 
 @pytest.mark.parametrize("carry,raw", [(False, False), (True, True)], ids=["zero", "carry"])
