@@ -11,8 +11,13 @@
 //   gx_k = sum_j w[K-1-j] gs_{k+j}             k + j inside the sequence
 //   gw[K-1-j] = sum_k gs_k x_{k-j},  gb = sum_k gs_k
 //
-// Both passes move each element once and do about ten operations on it, so HBM bounds them.  A
-// thread owns V = 4 neighbouring channels (1 where the channel count, a stride or an address does
+// Both passes move each element once.  Measured (bf16, 4352 channels, width 4): forward 16384 tokens 62 us,
+// 4.6 TB/s, 0.71 of the copy rate; backward 16001 tokens 126 us, 3.3 TB/s, 0.51.  Past the bytes it is
+// issue slots that bound them: 15 instructions an element forward and 30 backward, two of them on the
+// quarter-rate unit (ex2, rcp).  Not faster: two channels a thread instead of four, more resident warps
+// with 128 registers (backward 134 us), unpaired multiply-adds (66 and 131 us).
+//
+// A thread owns V = 4 neighbouring channels (1 where the channel count, a stride or an address does
 // not allow 8- or 16-byte accesses) and walks a run of the packed rows with its taps and a sliding
 // window of inputs in registers; the next rows are loaded before the present ones are computed.
 // Runs are cut along the packed rows, not along the sequences: every CTA has the same work whatever

@@ -21,6 +21,11 @@
 // of the group's first CTA issues the MMAs (N 256, K 16), warps 2-5 (2-9 with the activation's
 // gradient) drain one 256-column TMEM accumulator while the other fills, each warp storing its own 32
 // rows through its own staging boxes.
+// Measured (8177 tokens, d_model 2048, d_ff 8192; bf16 cuBLAS rate 1663 TFLOP/s in a burst, 1390 sustained
+// under the power cap): forward 670 us, 1.23 PFLOP/s; backward 1.62 ms, 1.02 PFLOP/s; on a cool card the
+// projections kernel 404 us, 1.36 PFLOP/s.  The two operands' way from L2 is what is left (10.7 TB/s at
+// 1.4 PFLOP/s): prefetching into L2 ahead of the loads made it 35 % slower, and other orders of the tiles
+// changed nothing.  Products with few tiles lose to the last wave (256 tiles on 74 pairs: 0.86).
 // An operand may lie along K (K-major: rows of 64 k, the descriptor's usual form) or across it
 // (MN-major: 64 x 64 boxes, 64 rows or columns wide), so nothing is transposed in memory.  Edges of
 // any size come out of the tensor maps: loads outside a matrix read zero, stores there are dropped.

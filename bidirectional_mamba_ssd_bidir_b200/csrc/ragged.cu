@@ -7,7 +7,8 @@
 // The recurrence is evaluated as written, token by token, with the state in registers: thread
 // (pg, nl) of a CTA holds P/16 rows x N/8 columns of it.  A step is about 3 P N / 128 fused
 // multiply-adds a thread and a reduction of y over the 8 column lanes, so issue slots bound the
-// kernel, not HBM.  Sequences are cut into segments of `seg` tokens when there are too few of them:
+// kernel, not HBM (8 heads of 32 x 64, 7 sequences of 533 tokens in all, float32: 21 us, 33 with one token at
+// a time and segments of 64).  Sequences are cut into segments of `seg` tokens when there are too few of them:
 // a first launch forms each segment's end state from zero (the sequence's own start state for its
 // first segment) and its decay; the second starts every segment from the states folded before it.
 // (The recurrence is linear in its state.)

@@ -40,19 +40,25 @@
 // sums along tokens.
 //
 // Warps: 0-7 make P and y, 8-15 the state and w x (TMEM lane quarter w & 3; w >> 2 & 1: two of P's four
-// column blocks, or the head), 16 the TMA loads, 17 to 19 the MMAs: an MMA of N = 128 runs for 32 cycles
-// but takes a thread some 100 to issue, so one issuing warp for the 48 of a chunk would bound it.
-// The two groups run at their own pace.  Group one: P_j, then y of the chunk before, so that the
-// products of chunk j run meanwhile.  Group two: S from the product of chunk j, its bf16 copy for chunk
-// j + 1, D x / rho of chunk j + 1, and, once P X of chunk j has read w x, w x of chunk j + 1.  Registers: a state warp holds 64
-// columns of S, so the groups are given 88 and 120 a thread and the last warpgroup 56
-// (128 (2 x 88 + 2 x 120 + 56) = 60416 of the 61440 launched with).
+// column blocks, or the head), 16 the TMA loads, 17 to 19 the MMAs, by what they wait for.  The two
+// groups run at their own pace.  Group one: P_j, then y of the chunk before, so that the products of
+// chunk j run meanwhile.  Group two: S from the product of chunk j, its bf16 copy for chunk j + 1,
+// D x / rho of chunk j + 1.  Each half of w x of chunk j + 1 once the products of chunk j have read theirs.
+// Registers: a state warp holds 64 columns of S, so the groups are given 88 and 120 a thread and the last
+// warpgroup 56 (128 (2 x 88 + 2 x 120 + 56) = 60416 of the 61440 launched with).
+//
+// What bounds it.  About 4.2 us a chunk and head pair (128 tokens; 32 KB of x and of y, 0.75 us at the
+// HBM's share of an SM).  The products' operands alone take shared memory 3.3 K of the 8 K cycles (56
+// products of 8 KB; 16 in a row were seen to take 1096 cycles), the passes of the two groups about 4 K
+// each, and what ties them is a chain: products read w x -> w x of the next chunk (0.9 K) -> its products
+// (1.6 K) -> S (0.7 K).  Tried and not kept: one issuing warp for all products and one group of 16
+// warps for all passes (12 K cycles a chunk), waits without the suspend hint (10 % slower), a second
+// stage of B instead of the third term (no faster).
 //
 // Rows past the segment's end (another sequence's, or none) are zeroed in x and B before a product
 // sees them, so nothing of theirs, NaN included, enters; their y rows are not written.
 //
-// STATES: the first of two launches when there are several segments: only w x and S, the state each
-// segment adds and its decay.
+// With several segments k_ragged_states comes first: the state that each segment adds and its decay.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -71,14 +77,14 @@ constexpr uint32_t kBox = 128 * 128;                   // 128 rows of 64 bf16: 1
 constexpr int kGroup = 8;                              // warps of a group
 
 // shared memory: everything but the tables in 16 KB boxes; 227 KB in all
-constexpr uint32_t kSX = 0;                            // x of two heads (STATES: a second stage where C is otherwise)
+constexpr uint32_t kSX = 0;                            // x of two heads
 constexpr uint32_t kSW = 2 * kBox;                     // w x: three terms of two heads each
 constexpr uint32_t kSB = 8 * kBox, kSC = 10 * kBox;    // B, C: two 64-column boxes each
 constexpr uint32_t kSS = 12 * kBox;                    // bf16 S: rows n, a box per head
 // One chunk and head's table: the column factors, which every warp reads (copied to shared memory):
 // q of the diagonal blocks, then of row blocks 1, 2, 3 (32, 64 and 96 columns); cs_b of the row blocks,
-// the chunk's decay, the steep blocks' bits,
-// m, and 0 in the long form or 1 + m - c.  Then per-row values.
+// the chunk's decay, the steep blocks' bits, m, and 0 in the long form or 1 + m - c.  Then per-row values.
+// The short form reads rho, w and the scalars alone, and only they are written for it.
 constexpr int kTabQd = 0, kTabQ = 128, kTabRef = 320, kTabTot = 324, kTabSteep = 325, kTabM = 326, kTabShort = 327, kTabShared = 328;
 constexpr int kTabRho = 328, kTabW = 456, kTabCs = 584, kTabCsd = 712, kTabLen = 840;   // kTabRho: log2 rho
 constexpr float kSteepBlock = 60.f, kSteepChunk = 150.f;
@@ -86,7 +92,7 @@ static_assert(kTabLen == kRaggedTable, "");
 constexpr uint32_t kTab = 14 * kBox;                   // q of both heads
 constexpr uint32_t kBars = kTab + 2 * kTabShared * 4;
 enum TcBar {
-    XF = 0, XF1, XE, XE1, BF, BF1, BE, BE1, CF, CE, TF, // loads: full / empty (x: two stages in STATES only); tables
+    XF = 0, XE, BF, BF1, BE, BE1, CF, CE, TF,          // loads: full / empty; the tables
     PREP, PREP1,                                       // w x written (even and odd chunks)
     SC, ST, ST1, YI, YF0, YF1,                         // products done: scores, new S (even and odd), C S^T, y (by buffer)
     PR, PR1, SB, YB, YE0, YE1,                         // P written; S's copy; D x / rho; y read (by buffer)
@@ -222,7 +228,6 @@ template <int R> __device__ __forceinline__ void regs_down() { asm volatile("set
 
 constexpr int kTcThreads = 640;
 
-template <bool STATES>
 __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_constant__ TcMaps maps,
                                                              const __grid_constant__ RaggedArgs a) {
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -237,9 +242,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
     // the ones before, it reads behind the wait.  (Every CTA waits, so that the next launch's wait covers all.)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Segment sg = find_segment(a.seq, a.seg, u);
-    if (blockIdx.x == 0 && !STATES) check_offsets(a.seq, a.status);
+    if (blockIdx.x == 0) check_offsets(a.seq, a.status);
     const bool last = sg.k == sg.count - 1;
-    if (sg.s < 0 || (STATES && last)) {                // the same for the whole CTA, before any allocation
+    if (sg.s < 0) {                                    // the same for the whole CTA, before any allocation
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
         *reinterpret_cast<volatile long long *>(abort_flag + 1) = a.wait_cycles;
         for (int i = 0; i < kNumBars; ++i) {
             const bool group = i == PR || i == PR1 || i == SB || i == YB || i == YE0 || i == YE1;
-            mbar_init(bar(i), (i == PREP || i == PREP1 || i == XE || i == XE1) ? 2 * kGroup : group ? kGroup : i == DONE ? 3 : ((i == BE || i == BE1) && !STATES) ? 2 : 1);
+            mbar_init(bar(i), (i == PREP || i == PREP1 || i == XE) ? 2 * kGroup : group ? kGroup : i == DONE ? 3 : (i == BE || i == BE1) ? 2 : 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -277,7 +282,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
     auto weigh = [&](int j, int row, int hh, int side, float w) {
         const int n = rows(j);
         const bool mine = a.dir > 0 ? row < n : row >= kQ - n;
-        const uint8_t *x = sm + (STATES && j & 1 ? kSC : kSX) + hh * kBox;
+        const uint8_t *x = sm + kSX + hh * kBox;
         uint8_t *to = sm + kSW + hh * kBox;
         const float2 w2 = make_float2(w, w), m1 = make_float2(-1.f, -1.f);
 #pragma unroll
@@ -302,24 +307,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
         fence_async_smem();
         __syncwarp();
     };
-    // STATES, group one: its half of w x
-    auto side_states = [&]() {
-        const int row = 32 * (warp & 3) + lane, hh = warp >> 2;
-        const float *t = a.tables + ((size_t)chunk0 * a.H + h0 + hh) * kTabLen + kTabW + row;
-        float w = nc > 0 ? *t : 0.f;
-        for (int j = 0; j < nc; ++j) {
-            const float now = w;
-            t += (size_t)a.H * kTabLen;
-            if (j + 1 < nc) w = *t;
-            // the product of the chunk before has read w x
-            if (!wait(XF + (j & 1), j >> 1, 191) || (j >= 1 && !wait(ST + ((j - 1) & 1), (j - 1) >> 1, 192))) break;
-            weigh(j, row, hh, 1, now);
-            if (lane == 0) {
-                mbar_arrive(bar(PREP + (j & 1)));
-                mbar_arrive(bar(XE + (j & 1)));
-            }
-        }
-    };
     if (warp >= 16) regs_down<56>();
     if (warp == 16) {
         // ------------------------------------------------------------ loads
@@ -330,17 +317,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
             float next = nc > 0 ? *tg : 0.f;
             for (int j = 0; j < nc; ++j) {
                 const int r = base(j);
-                const int st = STATES ? j & 1 : 0;
-                if (STATES ? j >= 2 && !wait1(XE + st, (j >> 1) - 1, 151) : j >= 1 && !wait1(XE, j - 1, 151)) break;
-                mbar_expect_tx(bar(XF + st), 2 * kBox);
-                for (int h = 0; h < 2; ++h) tma_load_2d(sbase + (st ? kSC : kSX) + h * kBox, &maps.x, 64 * (h0 + h), r, bar(XF + st));
+                if (j >= 1 && !wait1(XE, j - 1, 151)) break;
+                mbar_expect_tx(bar(XF), 2 * kBox);
+                for (int h = 0; h < 2; ++h) tma_load_2d(sbase + kSX + h * kBox, &maps.x, 64 * (h0 + h), r, bar(XF));
                 nx = j + 1;
                 if (j >= 1 && !wait1(BE + ((j - 1) & 1), (j - 1) >> 1, 152)) break;
                 mbar_expect_tx(bar(BF + (j & 1)), 2 * kBox);
                 for (int h = 0; h < 2; ++h)
                     tma_load_2d(sbase + kSB + h * kBox, &maps.b, 128 * grp + 64 * h, r, bar(BF + (j & 1)));
                 nb = j + 1;
-                if (STATES) continue;
                 if (j >= 1 && !wait1(CE, j - 1, 153)) break;
                 mbar_expect_tx(bar(CF), 2 * kBox);
                 for (int h = 0; h < 2; ++h) tma_load_2d(sbase + kSC + h * kBox, &maps.c, 128 * grp + 64 * h, r, bar(CF));
@@ -363,8 +348,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
                 ++nt;
             }
             if (*abort_flag) {                         // copies in flight land before the memory is given up
-                for (int j = nx - 1; j >= 0 && j >= nx - (STATES ? 2 : 1); --j)
-                    mbar_drain(bar(XF + (STATES ? j & 1 : 0)), (uint32_t)(STATES ? j >> 1 : j) & 1, a.wait_cycles);
+                if (nx) mbar_drain(bar(XF), (uint32_t)(nx - 1) & 1, a.wait_cycles);
                 if (nb) mbar_drain(bar(BF + ((nb - 1) & 1)), (uint32_t)((nb - 1) >> 1) & 1, a.wait_cycles);
                 if (ncc) mbar_drain(bar(CF), (uint32_t)(ncc - 1) & 1, a.wait_cycles);
                 if (nt) mbar_drain(bar(TF), (uint32_t)(nt - 1) & 1, a.wait_cycles);
@@ -373,7 +357,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
         __syncwarp();
     } else if (warp == 17) {
         // ------------------------------------------------------------ products that read C: scores, C S^T
-        if (!STATES) {
+        {
             const uint32_t id_sc = idesc(128, 0, 0), id_yi = idesc(128, 0, 1);
             const SDesc dC = make_sdesc(sbase + kSC, 16, 1024), dBk = make_sdesc(sbase + kSB, 16, 1024), dS = make_sdesc(sbase + kSS, kBox, 1024);
             const float *tg = a.tables + ((size_t)chunk0 * a.H + h0) * kTabLen + kTabShort;
@@ -436,7 +420,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
         __syncwarp();
     } else if (warp == 19) {
         // ------------------------------------------------------------ P X
-        if (!STATES) {
+        {
             const uint32_t id_px = idesc(64, 0, 1), id_pw = idesc(128, 0, 1);
             const SDesc dX = make_sdesc(sbase + kSX, kBox, 1024), dW = make_sdesc(sbase + kSW, kBox, 1024);
             const float *tg = a.tables + ((size_t)chunk0 * a.H + h0) * kTabLen + kTabShort;
@@ -471,9 +455,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
     } else if (warp < kGroup) {
         // ------------------------------------------------------------ P and y
         regs_down<88>();
-        if constexpr (STATES) {
-            side_states();
-        } else {
+        {
             const int q = warp & 3, hh = warp >> 2, h = h0 + hh, row = 32 * q + lane;
             const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
             const float *tab = reinterpret_cast<const float *>(sm + kTab);
@@ -684,25 +666,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
         {
             const float *in = nullptr;
             if (sg.k == 0) {
-                if (STATES || last) {
+                if (last) {
                     const int si = slot_of_start(a.slots, sg.s, a.status);
                     if (si >= 0) in = static_cast<const float *>(a.slots.pool_in) + (size_t)si * a.H * PN;
                 } else {
                     in = a.ws_state + (size_t)(u + sg.count - 1) * a.H * PN;
                 }
-            } else if (!STATES) {
+            } else {
                 in = a.ws_state + (size_t)(u - sg.k) * a.H * PN;
             }
 #pragma unroll
             for (int i = 0; i < 64; ++i) S[i] = in ? in[at + i * 128] : 0.f;
-            if (STATES && sg.k == 0) {
-                // the sequence's start, kept where its last segment's own state would be (nothing reads that)
-                float *keep = a.ws_state + (size_t)(u + sg.count - 1) * a.H * PN;
-#pragma unroll
-                for (int i = 0; i < 64; ++i) keep[at + i * 128] = S[i];
-            }
-            if (!STATES)
-                for (int k = 1; k < sg.k; ++k) {
+            for (int k = 1; k < sg.k; ++k) {
                     const size_t v = (size_t)(u - sg.k + k) * a.H;
                     const float d = ex2_ftz(a.ws_decay[v + h]);
                     const float *add = a.ws_state + v * PN + at;
@@ -711,7 +686,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
                 }
         }
         // Of the chunk that is next: w and log2 rho of this row, c and m (log2), its form
-        float wr = 0.f, lr = 0.f, tot = 0.f, ref = 0.f, total = 0.f;
+        float wr = 0.f, lr = 0.f, tot = 0.f, ref = 0.f;
         float shortness = 0.f;                         // kTabShort
         bool small = false;
         const float Dh = a.D ? a.D[h] : 0.f;
@@ -745,14 +720,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
         uint8_t *xb = sm + kSX + hh * kBox;
         // chunk j has landed; rows of no token: zero in x (the long form's product reads it) and B
         auto land = [&](int j) -> bool {
-            if (!wait(XF + (STATES ? j & 1 : 0), STATES ? j >> 1 : j, 163)) return false;
+            if (!wait(XF, j, 163)) return false;
             const int n = rows(j);
             if (n < kQ) {
                 if (!wait(BF + (j & 1), j >> 1, 164)) return false;
                 if (a.dir > 0 ? row >= n : row < kQ - n)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        if (!STATES) *reinterpret_cast<uint4 *>(xb + swz(row, i)) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4 *>(xb + swz(row, i)) = make_uint4(0u, 0u, 0u, 0u);
                         *reinterpret_cast<uint4 *>(sm + kSB + hh * kBox + swz(row, i)) = make_uint4(0u, 0u, 0u, 0u);
                     }
             }
@@ -788,16 +763,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
             weigh(j, row, hh, 0, wr);
             if (lane == 0) {
                 mbar_arrive(bar(PREP + (j & 1)));
-                if (STATES) mbar_arrive(bar(XE + (j & 1)));
-                else if (small) mbar_arrive(bar(XE));  // the long form's product reads x itself
+                if (small) mbar_arrive(bar(XE));  // the long form's product reads x itself
             }
         };
         bool ok = true;
         if (nc > 0) {
             load_w(0);
-            if (!STATES) copy_state();
+            copy_state();
             if ((ok = land(0))) {
-                if (!STATES) start_y(0);
+                start_y(0);
                 prepare(0);
             }
         }
@@ -805,7 +779,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
         for (int j = 0; j < nc && ok; ++j) {
             const float kappa = ex2_ftz(tot), add = small ? ex2_ftz(1.f - shortness) : 1.f;
             const bool was_small = small;
-            total += tot;
             if (j + 1 < nc) load_w(j + 1);
             if (!(ok = wait(ST + (j & 1), j >> 1, 168))) break;
             tc_fence_after();
@@ -823,32 +796,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
             }
             tc_fence_before();
             if (j + 1 == nc) break;
-            if (!STATES) {
-                if (!(ok = wait(YI, j, 169))) break;   // C S^T has read the copy it is written over
-                copy_state();
-                if (!was_small) {                      // P x of the long form has read x
-                    if (!(ok = wait(YF0 + (j & 1), j >> 1, 178))) break;
-                    if (lane == 0) mbar_arrive(bar(XE));
-                }
-                // the buffer of y is free: the y before last has been read (and the long form's C S^T there)
-                if ((j >= 1 && !(ok = wait(YE0 + ((j - 1) & 1), (j - 1) >> 1, 179))) ||
-                    (!was_small && !(ok = wait(YE0 + (j & 1), j >> 1, 180))))
-                    break;
-                tc_fence_after();
-                if (!(ok = land(j + 1))) break;
-                start_y(j + 1);
-                if (was_small && !(ok = wait(YF0 + (j & 1), j >> 1, 176))) break;   // P X has read w x
-            } else if (!(ok = land(j + 1))) {
-                break;
+            if (!(ok = wait(YI, j, 169))) break;   // C S^T has read the copy it is written over
+            copy_state();
+            if (!was_small) {                      // P x of the long form has read x
+                if (!(ok = wait(YF0 + (j & 1), j >> 1, 178))) break;
+                if (lane == 0) mbar_arrive(bar(XE));
             }
+            // the buffer of y is free: the y before last has been read (and the long form's C S^T there)
+            if ((j >= 1 && !(ok = wait(YE0 + ((j - 1) & 1), (j - 1) >> 1, 179))) ||
+                (!was_small && !(ok = wait(YE0 + (j & 1), j >> 1, 180))))
+                break;
+            tc_fence_after();
+            if (!(ok = land(j + 1))) break;
+            start_y(j + 1);
+            if (was_small && !(ok = wait(YF0 + (j & 1), j >> 1, 176))) break;   // P X has read w x
             prepare(j + 1);
         }
         if (ok) {
             float *out = nullptr;
-            if (STATES) {
-                out = a.ws_state + (size_t)u * a.H * PN;
-                if (q == 0 && lane == 0) a.ws_decay[(size_t)u * a.H + h] = total;
-            } else if (last && a.slots.pool_out) {
+            if (last && a.slots.pool_out) {
                 // (slot_of_end meets at a CTA barrier: its look for a second writer is done warp by warp here)
                 const int v = a.slots.out ? a.slots.out[sg.s] : sg.s;
                 bool good = v >= 0 && v < a.slots.n_out;
@@ -876,11 +842,205 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
     }
 }
 
-bool map_rows(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint64_t ld) {
+// ------------------------------------------------------------------ the segments' own states
+
+// S of every segment but a sequence's last, from zero (the first segment: from the sequence's start
+// state): the update above and nothing else.  Its products take half a chunk at a time (64 tokens), so
+// that the next half is weighed while they run: 16 warps weigh, two buffers of w x, three stages of x and
+// B, two accumulators; a chunk's sum is added to S while the next chunk's first half is multiplied.
+// A segment of this kernel has whole chunks only.  One sequence of 32741 tokens, 64 heads: 105 us, 125 as a
+// walk of whole chunks; x alone is 42 us at the HBM rate, the products' operand reads 50.
+constexpr int kHalf = 64, kStThreads = 576;
+constexpr uint32_t kHBox = kHalf * 128;                // 64 rows of 64 bf16: 8 KB
+constexpr uint32_t kTX = 0, kTB = 6 * kHBox, kTW = 12 * kHBox;   // x, B: three stages of two boxes; w x: two of six
+constexpr uint32_t kTBars = 24 * kHBox;
+enum StBar { HF = 0, HXE = 3, HBE = 6, HP = 9, HM = 11, HA = 13, HR = 15, HDONE = 17, kStBars };   // full; x, B empty; weighed; multiplied; sum full / read
+constexpr uint32_t kTMisc = (kTBars + kStBars * 8 + 15) & ~15u, kStSmem = kTMisc + 32;
+static_assert(kStSmem <= 232448, "shared memory budget");
+
+struct StMaps {
+    CUtensorMap x, b;
+};
+
+__global__ void __launch_bounds__(kStThreads, 1) k_ragged_states(const __grid_constant__ StMaps maps,
+                                                                 const __grid_constant__ RaggedArgs a) {
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const uint32_t sbase = smem_u32(sm);
+    auto bar = [&](int i) { return sbase + kTBars + 8u * i; };
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kTMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + kTMisc + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t MASK = 0xffffffffu;
+    const int pairs = a.H / 2, u = blockIdx.x / pairs, h0 = 2 * (blockIdx.x % pairs), grp = h0 / (a.H / a.G);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Segment sg = find_segment(a.seq, a.seg, u);
+    if (sg.s < 0 || sg.k == sg.count - 1 || (sbase & 1023)) {   // (a misaligned base is reported by k_ragged_tc)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
+    const int t0 = sg.k * a.seg, nc = a.seg / kQ, nh = 2 * nc;
+    const int chunk0 = chunk_number(sg, a.seg, 0);
+    // first row of half i: halves in the order of the rows, chunks in scan order
+    auto base = [&](int i) {
+        const int j = i >> 1;
+        return (a.dir > 0 ? sg.lo + t0 + j * kQ : sg.lo + sg.len - t0 - (j + 1) * kQ) + kHalf * (i & 1);
+    };
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        *reinterpret_cast<volatile long long *>(abort_flag + 1) = a.wait_cycles;
+        for (int i = 0; i < kStBars; ++i)
+            mbar_init(bar(i), (i >= HXE && i < HBE) || (i >= HP && i < HM) || (i >= HR && i < HDONE) ? 16 : 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 17) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_u32(tmem_slot)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t tmem = *tmem_slot;
+    auto wait = [&](int b, int phase, int code) { return mbar_wait(bar(b), (uint32_t)phase & 1, MASK, abort_flag, a.status, code); };
+
+    if (warp == 16) {
+        if (lane == 0) {
+            auto wait1 = [&](int b, int phase, int code) { return mbar_wait(bar(b), (uint32_t)phase & 1, 1u, abort_flag, a.status, code); };
+            int n = 0;
+            for (int i = 0; i < nh; ++i) {
+                const int st = i % 3, r = base(i);
+                if (i >= 3 && (!wait1(HXE + st, i / 3 - 1, 201) || !wait1(HBE + st, i / 3 - 1, 202))) break;
+                mbar_expect_tx(bar(HF + st), 4 * kHBox);
+                for (int h = 0; h < 2; ++h) {
+                    tma_load_2d(sbase + kTX + (2 * st + h) * kHBox, &maps.x, 64 * (h0 + h), r, bar(HF + st));
+                    tma_load_2d(sbase + kTB + (2 * st + h) * kHBox, &maps.b, 128 * grp + 64 * h, r, bar(HF + st));
+                }
+                n = i + 1;
+            }
+            if (*abort_flag)                           // copies in flight land before the memory is given up
+                for (int i = n - 1; i >= 0 && i >= n - 3; --i) mbar_drain(bar(HF + i % 3), (uint32_t)(i / 3) & 1, a.wait_cycles);
+        }
+        __syncwarp();
+    } else if (warp == 17) {
+        const uint32_t id = idesc(128, 1, 1);
+        for (int i = 0; i < nh; ++i) {
+            const int st = i % 3, j = i >> 1;
+            if (!wait(HP + (i & 1), i >> 1, 203) || !wait(HF + st, i / 3, 204) ||
+                (!(i & 1) && j >= 2 && !wait(HR + (j & 1), (j >> 1) - 1, 205)))
+                break;
+            tc_fence_after();
+            const SDesc db = make_sdesc(sbase + kTB + 2 * st * kHBox, kHBox, 1024), dw = make_sdesc(sbase + kTW + 6 * (i & 1) * kHBox, kHBox, 1024);
+            if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < 12; ++ks)
+                    mma_ss(tmem + 128 * (j & 1), db.at((ks & 3) * 2048), dw.at((ks >> 2) * 2 * kHBox + (ks & 3) * 2048), id, ks > 0 || (i & 1));
+                mma_commit(bar(HM + (i & 1)));
+                mma_commit(bar(HBE + st));
+                if (i & 1) mma_commit(bar(HA + (j & 1)));
+            }
+            __syncwarp();
+        }
+        if (elect_one()) mma_commit(bar(HDONE));
+        if (lane == 0) mbar_drain(bar(HDONE), 0, a.wait_cycles);
+        __syncwarp();
+    } else {
+        // S: n = 32 q + its lane, 32 columns (head, p) from 32 cg on; w x: row and 16 columns of a head
+        const int q = warp & 3, cg = warp >> 2, n = 32 * q + lane, hs = h0 + (cg >> 1);
+        const int hw = warp >> 3, row = 32 * (warp & 1) + lane, c0 = 2 * (warp >> 1 & 3);
+        const size_t PN = 64 * 128, at = (size_t)hs * PN + (size_t)(32 * (cg & 1)) * 128 + n;
+        float S[32];
+        const int si = sg.k == 0 ? slot_of_start(a.slots, sg.s, a.status) : -1;
+        const float *in = si >= 0 ? static_cast<const float *>(a.slots.pool_in) + (size_t)si * a.H * PN + at : nullptr;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) S[i] = in ? in[i * 128] : 0.f;
+        if (sg.k == 0) {
+            // the sequence's start, kept where its last segment's own state would be (nothing reads that):
+            // by the time the scan starts from it the pool may hold the sequence's new state
+            float *keep = a.ws_state + (size_t)(u + sg.count - 1) * a.H * PN + at;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) keep[i * 128] = S[i];
+        }
+        const size_t step = (size_t)a.H * kTabLen;
+        const float *tw = a.tables + ((size_t)chunk0 * a.H + h0 + hw) * kTabLen + kTabW + row;
+        const float *ts = a.tables + ((size_t)chunk0 * a.H + hs) * kTabLen;
+        float w = *tw, total = 0.f;
+        // S of chunk j
+        auto add_chunk = [&](int j) -> bool {
+            const float tot = ts[kTabTot], shortness = ts[kTabShort];
+            ts += step;
+            total += tot;
+            if (!wait(HA + (j & 1), j >> 1, 206)) return false;
+            tc_fence_after();
+            float ds[32];
+            tmem_ld32(tmem + ((uint32_t)(32 * q) << 16) + 128 * (j & 1) + 32 * cg, ds);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(HR + (j & 1)));
+            const float kappa = ex2_ftz(tot), add = shortness != 0.f ? ex2_ftz(1.f - shortness) : 1.f;
+            const float2 k2 = make_float2(kappa, kappa), a2 = make_float2(add, add);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float2 v = fma2(make_float2(S[i], S[i + 1]), k2, mul2(make_float2(ds[i], ds[i + 1]), a2));
+                S[i] = v.x;
+                S[i + 1] = v.y;
+            }
+            return true;
+        };
+        bool ok = true;
+        for (int i = 0; i < nh && ok; ++i) {
+            const int st = i % 3;
+            const float2 w2 = make_float2(w, w), m1 = make_float2(-1.f, -1.f);
+            if (i + 1 < nh) w = tw[((i + 1) >> 1) * step + kHalf * ((i + 1) & 1)];
+            // (this buffer's products of two halves ago)
+            if (!(ok = wait(HF + st, i / 3, 207) && (i < 2 || wait(HM + (i & 1), (i >> 1) - 1, 208)))) break;
+            const uint8_t *x = sm + kTX + (2 * st + hw) * kHBox;
+            uint8_t *to = sm + kTW + (6 * (i & 1) + hw) * kHBox;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const uint32_t off = swz(row, c0 + c);
+                const uint4 v = *reinterpret_cast<const uint4 *>(x + off);
+                const uint32_t xi[4] = {v.x, v.y, v.z, v.w};
+                uint32_t t[3][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float2 f = mul2(unpack2(xi[e]), w2);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        t[k][e] = pack_bf16(f.x, f.y);
+                        if (k < 2) f = fma2(unpack2(t[k][e]), m1, f);   // exact
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 3; ++k) *reinterpret_cast<uint4 *>(to + 2 * k * kHBox + off) = make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(bar(HP + (i & 1)));
+                mbar_arrive(bar(HXE + st));
+            }
+            if ((i & 1) && i > 1) ok = add_chunk((i >> 1) - 1);
+        }
+        if (ok && add_chunk(nc - 1)) {
+            float *out = a.ws_state + (size_t)u * a.H * PN + at;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) out[i * 128] = S[i];
+            if (q == 0 && (cg & 1) == 0 && lane == 0) a.ws_decay[(size_t)u * a.H + hs] = total;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 17) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem));
+    }
+}
+
+bool map_rows(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
     EncodeTiled enc = get_encode();
     if (!enc) return false;
     const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * 2};
-    const cuuint32_t box[2] = {64, 128}, estr[2] = {1, 1};
+    const cuuint32_t box[2] = {64, box_rows}, estr[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -899,7 +1059,7 @@ cudaError_t launch_ragged_tc(const RaggedArgs &a, cudaStream_t st) {
     TcMaps m;
     memset(&m, 0, sizeof m);
     const uint64_t T = a.seq.tokens, HP = 64ull * a.H, GN = 128ull * a.G;
-    if (!map_rows(&m.x, a.x, T, HP, a.ldx) || !map_rows(&m.b, a.B, T, GN, a.ldB) || !map_rows(&m.c, a.C, T, GN, a.ldC))
+    if (!map_rows(&m.x, a.x, T, HP, a.ldx, kQ) || !map_rows(&m.b, a.B, T, GN, a.ldB, kQ) || !map_rows(&m.c, a.C, T, GN, a.ldC, kQ))
         return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)(a.units * (a.H / 2));
     k_ragged_tables<<<dim3(a.seq.tokens / kQ + a.seq.nseq, (a.H + kTabHeads - 1) / kTabHeads), kTabThreads, 0, st>>>(a);
@@ -910,19 +1070,23 @@ cudaError_t launch_ragged_tc(const RaggedArgs &a, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kTcThreads);
-    cfg.dynamicSmemBytes = kTcSmem;
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
     if (a.seq.tokens > a.seg) {
-        e = cudaFuncSetAttribute(k_ragged_tc<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
-        if (e != cudaSuccess) return e;
-        if ((e = cudaLaunchKernelEx(&cfg, k_ragged_tc<true>, m, a)) != cudaSuccess) return e;
+        StMaps sm;
+        memset(&sm, 0, sizeof sm);
+        if (!map_rows(&sm.x, a.x, T, HP, a.ldx, kHalf) || !map_rows(&sm.b, a.B, T, GN, a.ldB, kHalf)) return cudaErrorInvalidValue;
+        if ((e = cudaFuncSetAttribute(k_ragged_states, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStSmem)) != cudaSuccess) return e;
+        cfg.blockDim = dim3(kStThreads);
+        cfg.dynamicSmemBytes = kStSmem;
+        if ((e = cudaLaunchKernelEx(&cfg, k_ragged_states, sm, a)) != cudaSuccess) return e;
     }
-    e = cudaFuncSetAttribute(k_ragged_tc<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = kTcSmem;
+    e = cudaFuncSetAttribute(k_ragged_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
     if (e != cudaSuccess) return e;
-    return cudaLaunchKernelEx(&cfg, k_ragged_tc<false>, m, a);
+    return cudaLaunchKernelEx(&cfg, k_ragged_tc, m, a);
 }
 
 }  // namespace ssd

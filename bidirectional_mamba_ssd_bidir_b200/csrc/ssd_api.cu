@@ -849,7 +849,10 @@ ssd_status ragged_plan(const ssd_ragged_shape *s, long long tokens, int nseq, Ra
     ssd_status st = check_heads(s->nheads, s->headdim, s->dstate, s->ngroups, s->io);
     if (st != SSD_OK) return st;
     if (tokens < 0 || nseq < 0 || tokens + nseq > 0x7fff0000LL) return fail(SSD_ERR_INVALID_ARG, "bad token or sequence count");
-    // Tensor-core shapes: one CTA (two heads) to an SM, chunks of 128 tokens; others: about four CTAs to an SM.
+    // Tensor-core shapes: one CTA (two heads) to an SM, chunks of 128 tokens, segments for about two CTAs an
+    // SM: longer ones leave SMs idle at the end, shorter ones start and fold more states (8 ragged prompts /
+    // one of 32741 tokens, 64 heads, us: one CTA an SM 410 / 528, two 350 / 503, three 349 / 531, six 362 / 650).
+    // Others: about four CTAs to an SM.
     const bool tc = s->io == SSD_BF16 && s->headdim == 64 && s->dstate == 128 && (s->nheads / s->ngroups) % 2 == 0;
     p->seg = tc ? ssd::ragged_segment(tokens, s->nheads / 2, 128, 2 * 148) : ssd::ragged_segment(tokens, s->nheads, 32, 4 * 148);
     p->units = (int)(tokens / p->seg) + nseq;
