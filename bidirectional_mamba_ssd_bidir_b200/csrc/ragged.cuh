@@ -17,7 +17,7 @@ namespace ssd {
 constexpr int kArgCode = 1000;
 constexpr int kCodeOffsets = 1001;    // cu_seqlens not ascending, or outside the packed rows
 constexpr int kCodeSlotRange = 1002;  // a slot index past the pool
-constexpr int kCodeSlotTwice = 1003;  // two sequences write the same slot
+constexpr int kCodeSlotTwice = 1003;  // a slot that one sequence (or row) writes and another uses
 
 // Sequences packed one after another: sequence i is rows [cu[i], cu[i+1]); cu == nullptr: each of
 // the nseq sequences has `len` rows.
@@ -163,8 +163,18 @@ __device__ __forceinline__ int slot_of_start(const Slots &s, int i, int *status)
     }
     return v < 0 ? -1 : v;
 }
-// Slot that sequence i ends in (-1: not stored).  Called by every thread of the CTA: a slot that a
-// second sequence names too is stored by neither.
+// Whether slot v, which sequence i is about to write, is another sequence's too: one that ends in it, or
+// starts from it in the same pool (and might read it before or after).  Looked at by `step` threads.
+__device__ __forceinline__ bool slot_shared(const Slots &s, int i, int nseq, int v, int first, int step) {
+    const bool starts = s.in && s.pool_in == s.pool_out, from_own = !s.in && s.pool_in == s.pool_out;
+    bool shared = from_own && v != i && v < nseq;
+    if (!s.out && !starts) return shared;
+    for (int j = first; j < nseq; j += step)
+        shared |= j != i && ((s.out && s.out[j] == v) || (starts && s.in[j] == v));
+    return shared;
+}
+// Slot that sequence i ends in (-1: not stored).  Called by every thread of the CTA: a slot that another
+// sequence uses too is not stored.
 __device__ __forceinline__ int slot_of_end(const Slots &s, int i, int nseq, int *status) {
     if (!s.pool_out) return -1;
     const int v = s.out ? s.out[i] : i;
@@ -173,10 +183,8 @@ __device__ __forceinline__ int slot_of_end(const Slots &s, int i, int nseq, int 
         report(status, kCodeSlotRange);
         return -1;
     }
-    if (!s.out) return v;
-    bool twice = false;
-    for (int j = threadIdx.x; j < nseq; j += blockDim.x) twice |= j != i && s.out[j] == v;
-    if (__syncthreads_or(twice)) {
+    if (!s.out && (!s.in || s.pool_in != s.pool_out)) return v;
+    if (__syncthreads_or(slot_shared(s, i, nseq, v, threadIdx.x, blockDim.x))) {
         report(status, kCodeSlotTwice);
         return -1;
     }

@@ -47,12 +47,12 @@
 // Registers: a state warp holds 64 columns of S, so the groups are given 88 and 120 a thread and the last
 // warpgroup 56 (128 (2 x 88 + 2 x 120 + 56) = 60416 of the 61440 launched with).
 //
-// What bounds it.  About 4.2 us a chunk and head pair (128 tokens; 32 KB of x and of y, 0.75 us at the
-// HBM's share of an SM).  The products' operands alone take shared memory 3.3 K of the 8 K cycles (56
-// products of 8 KB; 16 in a row were seen to take 1096 cycles), the passes of the two groups about 4 K
+// What bounds it.  4.1 to 4.7 us a chunk and head pair (128 tokens; 32 KB of x and of y, 0.75 us at the
+// HBM's share of an SM).  The products' operands alone take shared memory 2.8 K of the 8 K cycles (48
+// products, 8 KB each; 16 in a row were seen to take 1096 cycles), the passes of the two groups about 4 K
 // each, and what ties them is a chain: products read w x -> w x of the next chunk (0.9 K) -> its products
 // (1.6 K) -> S (0.7 K).  Tried and not kept: one issuing warp for all products and one group of 16
-// warps for all passes (12 K cycles a chunk), waits without the suspend hint (10 % slower), a second
+// warps for all passes (12 K cycles a chunk), waits without the suspend hint (3 to 5 % slower), a second
 // stage of B instead of the third term (no faster).
 //
 // Rows past the segment's end (another sequence's, or none) are zeroed in x and B before a product
@@ -815,17 +815,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
         if (ok) {
             float *out = nullptr;
             if (last && a.slots.pool_out) {
-                // (slot_of_end meets at a CTA barrier: its look for a second writer is done warp by warp here)
+                // (slot_of_end meets at a CTA barrier: its look for another user is done warp by warp here)
                 const int v = a.slots.out ? a.slots.out[sg.s] : sg.s;
                 bool good = v >= 0 && v < a.slots.n_out;
                 if (v >= a.slots.n_out) report(a.status, kCodeSlotRange);
-                if (good && a.slots.out) {
-                    bool twice = false;
-                    for (int i = lane; i < a.seq.nseq; i += 32) twice |= i != sg.s && a.slots.out[i] == v;
-                    if (__any_sync(MASK, twice)) {
-                        report(a.status, kCodeSlotTwice);
-                        good = false;
-                    }
+                if (good && __any_sync(MASK, slot_shared(a.slots, sg.s, a.seq.nseq, v, lane, 32))) {
+                    report(a.status, kCodeSlotTwice);
+                    good = false;
                 }
                 if (good) out = static_cast<float *>(a.slots.pool_out) + (size_t)v * a.H * PN;
             }
@@ -848,8 +844,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
 // state): the update above and nothing else.  Its products take half a chunk at a time (64 tokens), so
 // that the next half is weighed while they run: 16 warps weigh, two buffers of w x, three stages of x and
 // B, two accumulators; a chunk's sum is added to S while the next chunk's first half is multiplied.
-// A segment of this kernel has whole chunks only.  One sequence of 32741 tokens, 64 heads: 105 us, 125 as a
-// walk of whole chunks; x alone is 42 us at the HBM rate, the products' operand reads 50.
+// A segment of this kernel has whole chunks only.  One sequence of 32741 tokens, 64 heads: 135 us with cold
+// caches (2.1 TB/s); the whole call takes 483 us with it, 501 when this was a walk of whole chunks.  x alone
+// is 42 us at the HBM rate, the products' operand reads 50; a capture shows the tensor pipe 31 % active,
+// shared memory 35 % and issue slots 45 %, so what is left is the chain load, weigh, multiply of a half.
 constexpr int kHalf = 64, kStThreads = 576;
 constexpr uint32_t kHBox = kHalf * 128;                // 64 rows of 64 bf16: 8 KB
 constexpr uint32_t kTX = 0, kTB = 6 * kHBox, kTW = 12 * kHBox;   // x, B: three stages of two boxes; w x: two of six

@@ -380,7 +380,7 @@ ssd_status ssd_workspace_status(void *workspace, size_t workspace_bytes, void *s
         switch (word) {
             case ssd::kCodeOffsets: return fail(SSD_ERR_INVALID_ARG, "cu_seqlens not ascending, or outside the packed rows");
             case ssd::kCodeSlotRange: return fail(SSD_ERR_INVALID_ARG, "a slot index past the state pool");
-            case ssd::kCodeSlotTwice: return fail(SSD_ERR_INVALID_ARG, "two sequences or rows write one state slot");
+            case ssd::kCodeSlotTwice: return fail(SSD_ERR_INVALID_ARG, "a state slot that one sequence or row writes is used by another");
         }
         return fail(SSD_ERR_TIMEOUT, "a bounded device wait gave up (code %d)", word);
     }

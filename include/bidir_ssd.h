@@ -359,10 +359,11 @@ typedef struct {
  * means slot i.  pool_in and pool_out may be the same buffer, and a sequence
  * may end in the slot it started from; no other sequence of the call may start
  * from a slot that one of them writes.  An empty sequence passes its state
- * on.  A slot index past n_in / n_out counts as no slot, and a slot that two
- * sequences would write is written by neither; both are recorded in the
- * status word, as are offsets that are not ascending
- * (ssd_workspace_status then returns SSD_ERR_INVALID_ARG). */
+ * on.  A slot index past n_in / n_out counts as no slot, and a slot that
+ * another sequence of the call uses too is not written (two that would write
+ * it: by neither; pool_in == pool_out and another that starts from it: it
+ * keeps its state); both are recorded in the status word, as are offsets that
+ * are not ascending (ssd_workspace_status then returns SSD_ERR_INVALID_ARG). */
 typedef struct {
     const void *pool_in;
     void *pool_out;

@@ -485,6 +485,36 @@ def test_bad_indices_are_reported_and_skipped(ssd):
     assert bool((ssm == 0).all())
 
 
+def test_a_slot_another_sequence_starts_from_is_kept(ssd):
+    """A sequence may end in the slot it started from; a slot that another one starts from is left as it was
+    (which of the two came first would be up to the schedule), and the status word says so."""
+    g = _gen("kept")
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    # (slots_in, slots_out, slots that stay as they were)
+    cases = [(i32(0, 1), i32(1, 2), [0, 1, 3]), (i32(2, 0), i32(2, 0), [1, 3]), (None, i32(1, 3), [0, 1, 2]),
+             (i32(1, 2), None, [1, 2, 3])]
+
+    def check(call, start, nbytes):
+        for ins, outs, stay in cases:
+            pool, ws = start.clone(), torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+            call(state_in=pool, state_out=pool, slots_in=ins, slots_out=outs, workspace=ws)
+            assert [s for s in range(4) if torch.equal(pool[s], start[s])] == stay
+            if len(stay) == 2:
+                ssd.workspace_status(ws)
+            else:
+                with pytest.raises(ssd.SSDError, match="slot"):
+                    ssd.workspace_status(ws)
+
+    x, w = torch.randn(20, 8, generator=g).cuda(), torch.randn(8, 4, generator=g).cuda()
+    check(lambda **kw: ssd.ssd_conv(x, w, cu_seqlens=_cu([10, 10]), **kw), torch.randn(4, 3, 8, generator=g).cuda(), 256)
+    for dt, P, N, lens in ((torch.float32, 16, 16, [10, 10]), (torch.bfloat16, 64, 128, [130, 10])):
+        T = sum(lens)
+        xs, B = torch.randn(T, 2, P, generator=g).to(dt).cuda(), torch.randn(T, 1, N, generator=g).to(dt).cuda()
+        d, A = torch.rand(T, 2, generator=g).to(dt).cuda(), -torch.ones(2, device="cuda")
+        check(lambda **kw: ssd.ssd_scan_ragged(xs, d, A, B, B, cu_seqlens=_cu(lens), **kw),
+              torch.randn(4, 2, P, N, generator=g).cuda(), ssd.ragged_workspace_bytes(T, 2, 2, P, N, 1, dt))
+
+
 def test_graph_replays_follow_new_inputs(ssd):
     """A captured decoding step (padded batch, slots in a device tensor) replayed on new contents, and on a
     side stream."""
