@@ -80,6 +80,7 @@ struct RaggedArgs {
     int seg, units;                // tokens of a segment, segments at most
     float *ws_state, *ws_decay;    // [units][H][P][N] and [units][H]
     float *tables;                 // tensor-core form: [tokens / 128 + nseq][H][kRaggedTable]
+    int *order;                    // its jobs, longest first, and scratch: 2 [units][H / 2] (null: as they are numbered)
     int *status;
     long long wait_cycles;
 };
@@ -120,16 +121,21 @@ __device__ __forceinline__ int seq_find(const Packed &s, int t) {
 struct Segment {
     int s, k, count, lo, len;
 };
-// Called by whole warps: 32 starts are looked at together (a search one by one is a chain of loads, and a
-// kernel's first loads wait for it).
+// Called by whole warps: 32 starts are looked at together, one step for up to 32 sequences and two for 1024
+// (a search one by one is a chain of loads, and a kernel's first loads wait for it).
 __device__ __forceinline__ Segment find_segment(const Packed &q, int seg, int u) {
     const int lane = threadIdx.x & 31;
-    int lo = -1;                              // the last sequence with start / seg + number <= u
-    for (int b = 0; b < q.nseq; b += 32) {
-        const int n = __popc(__ballot_sync(0xffffffffu, b + lane < q.nseq && seq_start(q, b + lane) / seg + b + lane <= u));
-        lo += n;
-        if (n < 32) break;
+    // the last sequence with start / seg + number <= u: those before `lo` have it, m more may
+    int lo = 0;
+    for (int m = q.nseq; m > 0;) {
+        const int st = (m + 31) / 32, at = lane * st;
+        const int n = __popc(__ballot_sync(0xffffffffu, at < m && seq_start(q, lo + at) / seg + lo + at <= u));
+        if (n == 0) break;
+        const int skip = (n - 1) * st + 1;
+        lo += skip;
+        m = min(st - 1, m - skip);
     }
+    --lo;
     Segment r{-1, 0, 0, 0, 0};
     if (lo < 0) return r;
     r.lo = seq_start(q, lo);

@@ -841,7 +841,7 @@ ssd_status check_step(const ssd_step_shape *s) {
 
 struct RaggedPlan {
     int seg, units;
-    size_t state, decay, tables, total;     // workspace offsets and size
+    size_t state, decay, tables, order, total;     // workspace offsets and size
 };
 
 ssd_status ragged_plan(const ssd_ragged_shape *s, long long tokens, int nseq, RaggedPlan *p) {
@@ -851,7 +851,8 @@ ssd_status ragged_plan(const ssd_ragged_shape *s, long long tokens, int nseq, Ra
     if (tokens < 0 || nseq < 0 || tokens + nseq > 0x7fff0000LL) return fail(SSD_ERR_INVALID_ARG, "bad token or sequence count");
     // Tensor-core shapes: one CTA (two heads) to an SM, chunks of 128 tokens, segments for about two CTAs an
     // SM: longer ones leave SMs idle at the end, shorter ones start and fold more states (8 ragged prompts /
-    // one of 32741 tokens, 64 heads, us: one CTA an SM 410 / 528, two 350 / 503, three 349 / 531, six 362 / 650).
+    // one of 32741 tokens, 64 heads, us: one and a half CTAs an SM 274 / 584, two 291 / 486, two and a half
+    // 288 / 571, three 302 / 516, four 320 / 554).
     // Others: about four CTAs to an SM.
     const bool tc = s->io == SSD_BF16 && s->headdim == 64 && s->dstate == 128 && (s->nheads / s->ngroups) % 2 == 0;
     p->seg = tc ? ssd::ragged_segment(tokens, s->nheads / 2, 128, 2 * 148) : ssd::ragged_segment(tokens, s->nheads, 32, 4 * 148);
@@ -861,7 +862,8 @@ ssd_status ragged_plan(const ssd_ragged_shape *s, long long tokens, int nseq, Ra
     p->state = kStatusBytes;
     p->decay = p->state + round_up(n * s->headdim * s->dstate * sizeof(float));
     p->tables = p->decay + round_up(n * sizeof(float));
-    p->total = p->tables + (tc ? round_up((size_t)(tokens / 128 + nseq) * s->nheads * ssd::kRaggedTable * sizeof(float)) : 0);
+    p->order = p->tables + (tc ? round_up((size_t)(tokens / 128 + nseq) * s->nheads * ssd::kRaggedTable * sizeof(float)) : 0);
+    p->total = p->order + (tc ? round_up(n * sizeof(int)) : 0);
     return SSD_OK;
 }
 
@@ -945,6 +947,7 @@ ssd_status ssd_scan_ragged(const ssd_ragged_shape *shape, const ssd_packed *seq,
     a.ws_state = reinterpret_cast<float *>(ws + plan.state);
     a.ws_decay = reinterpret_cast<float *>(ws + plan.decay);
     a.tables = reinterpret_cast<float *>(ws + plan.tables);
+    a.order = a.seq.tokens > plan.seg ? reinterpret_cast<int *>(ws + plan.order) : nullptr;
     a.status = static_cast<int *>(workspace);
     a.wait_cycles = wait_cycles_now();
     const bool bf16 = shape->io == SSD_BF16;

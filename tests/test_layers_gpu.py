@@ -296,6 +296,34 @@ def test_scan_ragged_tensor_core_long(ssd, lens, H, G, direction, carry, steep):
     for i in range(S):
         _check(pool[i], last[i].cpu(), _tc_s(lens[i], last[i].cpu(), lastm[i].cpu()), f"state {i}")
 
+@pytest.mark.parametrize("P,N,io,direction", [(64, 128, "bf16", 1), (64, 128, "bf16", -1), (16, 16, "f32", 1)], ids=str)
+def test_scan_ragged_many_sequences(ssd, P, N, io, direction):
+    """More sequences than are looked at together, most of them empty or a token long, some of several segments."""
+    dt, H = (torch.bfloat16 if io == "bf16" else torch.float32), 2
+    lens = [(0, 1, 0, 2, 0)[i % 5] for i in range(1100)]
+    for i, n in ((0, 300), (31, 129), (32, 400), (511, 1), (700, 513), (1056, 256), (1099, 131)):
+        lens[i] = n
+    T, S = sum(lens), len(lens)
+    g = _gen("many", P, direction)
+    _, x, B, C, d, A, D, _ = _scan_inputs(g, T, H, P, N, 1, dt, False)
+    x, B, C, d, A, D = (v.contiguous().cuda() for v in (x, B, C, d, A, D))
+    pool = torch.randn(S, H, P, N, generator=g).cuda()
+    start = [pool[i].clone() for i in range(S)]
+    ws = torch.zeros(ssd.ragged_workspace_bytes(T, S, H, P, N, 1, dt), dtype=torch.uint8, device="cuda")
+    y = ssd.ssd_scan_ragged(x, d, A, B, C, D, cu_seqlens=_cu(lens), direction=direction, state_in=pool, state_out=pool,
+                            workspace=ws)
+    ssd.workspace_status(ws)
+    ref, ym, last, lastm = ol.scan(x, d, A, B, C, D, lens, None, direction, start)
+    ref, ym, last, lastm = ref.cpu(), ym.cpu(), torch.stack(list(last)).cpu(), torch.stack(list(lastm)).cpu()
+    if io == "bf16":
+        _check(y, ref, _tc_y(max(lens), N, ref, ym), "y")
+        _check(pool, last, _tc_s(max(lens), last, lastm), "states")
+    else:
+        n = max(lens)
+        _check(y, ref, HALF[dt] * ref.abs() + (1 + HALF[dt]) * (6 * n + 2 * N + 40) * U * ym + 1e-37, "y")
+        _check(pool, last, (6 * n + 40) * U * lastm + 1e-37, "states")
+
+
 def test_scan_ragged_neighbours_do_not_leak(ssd):
     """NaN and infinity in one sequence (and behind the last) leave the others bit for bit, states too."""
     g = _gen("leak")
