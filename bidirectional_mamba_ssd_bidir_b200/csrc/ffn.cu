@@ -8,9 +8,10 @@
 //
 // act = SiLU: g sg, act' = sg (1 + g (1 - sg)); or GELU: g Phi(g), act' = Phi(g) + g phi(g).
 //
-// Three launches forward and backward together do all of it: the two projections, the activation and
-// the product in one kernel (h, and the projections when they are saved); gh with the activation's
-// gradient in its epilogue; and the three remaining products of the backward pass side by side.
+// Two launches forward and two backward do all of it: the two projections, the activation and the
+// product in one (h, and the projections when they are saved), then out; gh with the activation's
+// gradient in its epilogue; and the three remaining products of the backward pass side by side (with few
+// tokens gu in a launch of its own).
 // Rounded to bf16 between them: h, gg, gp and the saved projections (the operands of the next
 // product have to be bf16 for the tensor core; accumulation, activation and its derivative are
 // float32).
@@ -483,7 +484,12 @@ __global__ void __launch_bounds__(kFfnThreads<EPI>, 1) k_ffn(const __grid_consta
 // Both forms measured at d_model 2048, d_ff 8192 (us, this one / the other): 3 tokens 26 / 99, 128: 40 /
 // 99, 256: 59 / 88, 512: 69 / 101, 1024: 120 / 126; at 768, 2048: 800 tokens 27 / 36.  Past 1024 tokens the
 // persistent tiles fill the SMs and hide their epilogues.
-constexpr int kFewMax = 1024;
+//
+// gu = [gg gp] W_in of the backward pass has the longest K (2 d_ff) and, with few tokens, next to no tiles: beside
+// the other two products it alone set the time.  Up to 2048 tokens it is a launch of this kernel, W_in
+// taken as it lies (MN-major).  The whole backward pass at d_model 2048, d_ff 8192 (us, so / all three side by
+// side): 16 tokens 81 / 172, 256: 119 / 181, 512: 124 / 196, 1024: 211 / 254, 1500: 310 / 324, 2048: 382 / 391.
+constexpr int kFewMax = 1024, kFewGrad = 2048;
 template <int N> struct FewTile {
     static constexpr uint32_t kW = 128 * 128, kU = N * 128, kStage = kW + kU;
     // two CTAs to an SM, or one of 256 tokens
@@ -498,6 +504,7 @@ struct FewParams {
     CUtensorMap w, u;
     int rows, K, T, up_row;        // rows of the output (d_ff or d_model); tokens
     int split, save, gelu, wait_prior;
+    int w_mn;                      // the weights lie [K][rows] (EPI_PLAIN)
     __nv_bfloat16 *out, *gu;       // out [T][rows]; gu [T][2 rows]
     int *status;
     long long wait_cycles;
@@ -540,6 +547,9 @@ __global__ void __launch_bounds__(kFThreads) k_ffn_few(const __grid_constant__ F
                 if (EPI == EPI_GLU) {
                     tma_load_2d(at, &prm.w, kt * kFK, kRows * tile, bar(st));
                     tma_load_2d(at + L::kW / 2, &prm.w, kt * kFK, prm.up_row + kRows * tile, bar(st));
+                } else if (prm.w_mn) {
+                    tma_load_2d(at, &prm.w, kRows * tile, kt * kFK, bar(st));
+                    tma_load_2d(at + L::kW / 2, &prm.w, kRows * tile + 64, kt * kFK, bar(st));
                 } else {
                     tma_load_2d(at, &prm.w, kt * kFK, kRows * tile, bar(st));
                 }
@@ -564,15 +574,16 @@ __global__ void __launch_bounds__(kFThreads) k_ffn_few(const __grid_constant__ F
         }
         __syncwarp();
     } else if (warp == 1) {
-        const uint32_t id = idesc(N, 0, 0);
+        const bool mn = EPI == EPI_PLAIN && prm.w_mn;              // (the layouts are k_ffn's)
+        const uint32_t id = idesc(N, mn, 0), lw = mn ? L::kW / 2 : 16, kw = mn ? 2048 : 32;
         for (int i = 0; i < k1 - k0; ++i) {
             const int st = i % S;
             if (!mbar_wait(bar(st), (uint32_t)(i / S) & 1, 0xffffffffu, abort_flag, prm.status, 182)) break;
             tc_fence_after();
             const uint32_t at = sbase + st * L::kStage;
-            const SDesc dw = make_sdesc(at, 16, 1024), du = make_sdesc(at + L::kW, 16, 1024);
+            const SDesc dw = make_sdesc(at, lw, 1024), du = make_sdesc(at + L::kW, 16, 1024);
 #pragma unroll
-            for (int ks = 0; ks < kFK / 16; ++ks) mma_ss_w(tmem, dw.at(ks * 32), du.at(ks * 32), id, (i | ks) != 0);
+            for (int ks = 0; ks < kFK / 16; ++ks) mma_ss_w(tmem, dw.at(ks * kw), du.at(ks * 32), id, (i | ks) != 0);
             mma_commit_w(bar(S + st));
         }
         mma_commit_w(bar(2 * S));
@@ -757,7 +768,8 @@ template <int EPI, int N> cudaError_t run_few(FewParams &prm, cudaStream_t st) {
 
 template <int EPI> cudaError_t run_few_any(FewParams &prm, const void *w, int w_rows, const void *u, cudaStream_t st) {
     const int n = prm.T <= 16 ? 16 : prm.T <= 32 ? 32 : prm.T <= 64 ? 64 : prm.T <= 128 ? 128 : 256;
-    if (!map_of(&prm.w, w, w_rows, prm.K, prm.K, EPI == EPI_GLU ? 64 : 128) || !map_of(&prm.u, u, prm.T, prm.K, prm.K, n))
+    if (!(prm.w_mn ? map_of(&prm.w, w, prm.K, w_rows, w_rows, 64) : map_of(&prm.w, w, w_rows, prm.K, prm.K, EPI == EPI_GLU ? 64 : 128)) ||
+        !map_of(&prm.u, u, prm.T, prm.K, prm.K, n))
         return cudaErrorInvalidValue;
     switch (n) {
         case 16: return run_few<EPI, 16>(prm, st);
@@ -824,18 +836,31 @@ cudaError_t launch_ffn_bwd(const FfnArgs &a, cudaStream_t st) {
         return cudaErrorInvalidValue;
     cudaError_t e = run_ffn_any<EPI_GLU_BWD>(prm, st);
     if (e != cudaSuccess) return e;
-    // the longest products first: their tiles end last otherwise
-    prm.nprob = 3;
     prm.wait_prior = 1;
-    prm.p[0] = product(a.T, a.D, 2 * a.F, false, true);
-    prm.p[1] = product(2 * a.F, a.D, a.T, true, true);
-    prm.p[2] = product(a.D, a.F, a.T, true, true);
-    if (!operand(&prm.p[0].a, ggu, a.T, 2 * a.F, false) || !operand(&prm.p[0].b, a.W_in, a.D, 2 * a.F, true) ||
-        !map_of(&prm.p[0].d[0], a.gu_, a.T, a.D, a.D, 32) ||
-        !operand(&prm.p[1].a, ggu, 2 * a.F, a.T, true) || !operand(&prm.p[1].b, a.u, a.D, a.T, true) ||
-        !map_of(&prm.p[1].d[0], a.gW_in, 2 * a.F, a.D, a.D, 32) ||
-        !operand(&prm.p[2].a, a.gy, a.D, a.T, true) || !operand(&prm.p[2].b, a.h, a.F, a.T, true) ||
-        !map_of(&prm.p[2].d[0], a.gW_out, a.D, a.F, a.F, 32))
+    prm.nprob = 0;
+    if (a.T <= kFewGrad) {
+        // gu has few tiles and the longest K: the form for few tokens splits it over the SMs
+        FewParams few;
+        memset(&few, 0, sizeof few);
+        few.rows = a.D; few.K = 2 * a.F; few.T = a.T; few.w_mn = 1; few.wait_prior = 1;
+        few.out = static_cast<__nv_bfloat16 *>(a.gu_);
+        few.status = a.status; few.wait_cycles = a.wait_cycles;
+        if ((e = run_few_any<EPI_PLAIN>(few, a.W_in, a.D, ggu, st)) != cudaSuccess) return e;
+    } else {
+        // the longest products first: their tiles end last otherwise
+        FfnProb &g = prm.p[prm.nprob++];
+        g = product(a.T, a.D, 2 * a.F, false, true);
+        if (!operand(&g.a, ggu, a.T, 2 * a.F, false) || !operand(&g.b, a.W_in, a.D, 2 * a.F, true) ||
+            !map_of(&g.d[0], a.gu_, a.T, a.D, a.D, 32))
+            return cudaErrorInvalidValue;
+    }
+    FfnProb &in = prm.p[prm.nprob++], &out = prm.p[prm.nprob++];
+    in = product(2 * a.F, a.D, a.T, true, true);
+    out = product(a.D, a.F, a.T, true, true);
+    if (!operand(&in.a, ggu, 2 * a.F, a.T, true) || !operand(&in.b, a.u, a.D, a.T, true) ||
+        !map_of(&in.d[0], a.gW_in, 2 * a.F, a.D, a.D, 32) ||
+        !operand(&out.a, a.gy, a.D, a.T, true) || !operand(&out.b, a.h, a.F, a.T, true) ||
+        !map_of(&out.d[0], a.gW_out, a.D, a.F, a.F, 32))
         return cudaErrorInvalidValue;
     return run_ffn_any<EPI_PLAIN>(prm, st);
 }

@@ -50,7 +50,8 @@ def _check(got, ref, tol, what):
 # tokens: one, a ragged pair of row tiles, more than one tile pair; sizes below, at and past the
 # 64 / 128 / 256 steps of the tiles
 SIZES = [(1, 8, 8), (1, 256, 512), (3, 64, 136), (17, 200, 1000), (64, 128, 128), (65, 136, 72), (128, 256, 256), (129, 264, 520),
-         (200, 512, 1160), (256, 64, 384), (300, 1000, 640), (515, 768, 264), (1000, 24, 2056), (2049, 136, 136)]
+         (200, 512, 1160), (256, 64, 384), (300, 1000, 640), (515, 768, 264), (1000, 24, 2056), (2049, 136, 136),
+         (40, 264, 4096), (130, 1032, 2048), (2048, 136, 72)]
 
 
 @pytest.mark.parametrize("T,D,F", SIZES)
