@@ -417,7 +417,10 @@ ssd_status ssd_conv_bwd(const ssd_conv_shape *shape, const ssd_packed *seq, cons
  * that are multiples of 16 bytes runs on the tensor cores in chunks of 128
  * tokens: scores, inputs and the copy of the state that meets C are rounded to
  * bf16 there; the state itself is float32, from products of three bf16 terms
- * (2^-25).  A NaN or an infinity in x, B, C or dt may reach the up to 127 tokens
+ * (2^-25).  Decays inside a chunk are differences of float32 sums along it: a
+ * term of y is off by a further 2^-22 or so of the chunk's whole decay (as log2),
+ * past bf16's rounding only where 128 tokens decay by more than 2^-16384 in all.
+ * A NaN or an infinity in x, B, C or dt may reach the up to 127 tokens
  * before its own in the same sequence; it never reaches another sequence. */
 typedef struct {
     int nheads, headdim, dstate, ngroups;
