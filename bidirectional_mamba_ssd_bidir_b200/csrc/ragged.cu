@@ -28,7 +28,8 @@ __global__ void __launch_bounds__(kThreads) k_ragged(const __grid_constant__ Rag
     constexpr int PPT = P / 16, NPT = N / 8, W = NPT < 4 ? NPT : 4, NQ = NPT / W;
     __shared__ float sx[kTB][P], sB[kTB][N], sC[kTB][N], sy[kTB][P], sdt[kTB], slog[kTB], sdec[kTB];
     const int u = blockIdx.x, h = blockIdx.y, g = h / (a.H / a.G);
-    const Segment sg = find_segment(a.seq, a.seg, u);
+    const Segment sg = STATES ? find_state(a.seq, a.seg, u) : find_segment(a.seq, a.seg, u);
+    const int v0 = first_state(sg, a.seg);
     if (u == 0 && h == 0 && !STATES) check_offsets(a.seq, a.status);
     if (sg.s < 0) return;
     const bool last = sg.k == sg.count - 1;
@@ -60,16 +61,16 @@ __global__ void __launch_bounds__(kThreads) k_ragged(const __grid_constant__ Rag
             if (STATES) {
                 // kept for the scan in the place of the sequence's last segment, whose own end state
                 // nothing reads: by then the pool may already hold the sequence's new state
-                float *keep = a.ws_state + ((size_t)(u + sg.count - 1) * a.H + h) * PN;
+                float *keep = a.ws_state + ((size_t)(v0 + sg.count - 1) * a.H + h) * PN;
                 each([&](float &s, size_t o) { keep[o] = s; });
             }
         } else {
-            const float *in = a.ws_state + ((size_t)(u + sg.count - 1) * a.H + h) * PN;
+            const float *in = a.ws_state + ((size_t)(v0 + sg.count - 1) * a.H + h) * PN;
             each([&](float &s, size_t o) { s = in[o]; });
         }
     } else if (!STATES) {
         for (int k = 0; k < sg.k; ++k) {
-            const size_t v = (size_t)(u - sg.k + k) * a.H + h;
+            const size_t v = (size_t)(v0 + k) * a.H + h;
             const float d = expf(a.ws_decay[v]);
             const float *in = a.ws_state + v * PN;
             each([&](float &s, size_t o) { s = (k == 0 ? 0.f : s * d) + in[o]; });
@@ -155,9 +156,8 @@ __global__ void __launch_bounds__(kThreads) k_ragged(const __grid_constant__ Rag
 }
 
 template <typename T, int P, int N> cudaError_t run_ragged(const RaggedArgs &a, cudaStream_t st) {
-    const dim3 grid(a.units, a.H);
-    if (a.seq.tokens > a.seg) k_ragged<T, P, N, true><<<grid, kThreads, 0, st>>>(a);   // some sequence may have two
-    k_ragged<T, P, N, false><<<grid, kThreads, 0, st>>>(a);
+    if (a.states) k_ragged<T, P, N, true><<<dim3(a.states, a.H), kThreads, 0, st>>>(a);
+    k_ragged<T, P, N, false><<<dim3(a.units, a.H), kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 

@@ -77,8 +77,9 @@ struct RaggedArgs {
     const float *A, *D, *dt_bias;  // D, dt_bias may be null
     void *y;
     int H, P, N, G, dir;
-    int seg, units;                // tokens of a segment, segments at most
-    float *ws_state, *ws_decay;    // [units][H][P][N] and [units][H]
+    int seg, units;                // tokens of a segment (even), segments at most
+    int states;                    // state numbers of the workspace (below); 0: no sequence has two segments
+    float *ws_state, *ws_decay;    // [states][H][P][N] and [states][H]
     float *tables;                 // tensor-core form: [tokens / 128 + nseq][H][kRaggedTable]
     int *order;                    // its jobs, longest first, and scratch: 2 [units][H / 2] (null: as they are numbered)
     int *status;
@@ -121,28 +122,51 @@ __device__ __forceinline__ int seq_find(const Packed &s, int t) {
 struct Segment {
     int s, k, count, lo, len;
 };
+// The last sequence i with before(start, i), which holds for a first part of them (-1: for none).
 // Called by whole warps: 32 starts are looked at together, one step for up to 32 sequences and two for 1024
 // (a search one by one is a chain of loads, and a kernel's first loads wait for it).
-__device__ __forceinline__ Segment find_segment(const Packed &q, int seg, int u) {
+template <typename F> __device__ __forceinline__ int last_sequence(const Packed &q, F before) {
     const int lane = threadIdx.x & 31;
-    // the last sequence with start / seg + number <= u: those before `lo` have it, m more may
-    int lo = 0;
+    int lo = 0;                               // those before `lo` have it, m more may
     for (int m = q.nseq; m > 0;) {
         const int st = (m + 31) / 32, at = lane * st;
-        const int n = __popc(__ballot_sync(0xffffffffu, at < m && seq_start(q, lo + at) / seg + lo + at <= u));
+        const int n = __popc(__ballot_sync(0xffffffffu, at < m && before(seq_start(q, lo + at), lo + at)));
         if (n == 0) break;
         const int skip = (n - 1) * st + 1;
         lo += skip;
         m = min(st - 1, m - skip);
     }
-    --lo;
-    Segment r{-1, 0, 0, 0, 0};
-    if (lo < 0) return r;
-    r.lo = seq_start(q, lo);
-    r.len = max(0, seq_start(q, lo + 1) - r.lo);
-    r.k = u - (r.lo / seg + lo);
+    return lo - 1;
+}
+__device__ __forceinline__ Segment segments_of(const Packed &q, int seg, int i) {
+    Segment r{i, 0, 0, seq_start(q, i), 0};
+    r.len = max(0, seq_start(q, i + 1) - r.lo);
     r.count = max(1, (r.len + seg - 1) / seg);
-    r.s = r.k >= 0 && r.k < r.count ? lo : -1;
+    return r;
+}
+__device__ __forceinline__ Segment find_segment(const Packed &q, int seg, int u) {
+    const int i = last_sequence(q, [&](int start, int i) { return start / seg + i <= u; });
+    if (i < 0) return Segment{-1, 0, 0, 0, 0};
+    Segment r = segments_of(q, seg, i);
+    r.k = u - (r.lo / seg + i);
+    if (r.k < 0 || r.k >= r.count) r.s = -1;
+    return r;
+}
+
+// States are kept between the launches for sequences of two or more segments alone: segment k of one that
+// starts at row lo has state number lo / half + k, half = seg / 2.  The numbers of different sequences differ:
+// with len > 2 half, ceil(len / seg) <= floor(len / half), and floor(lo / half) + floor(len / half) is at most the
+// next sequence's first number.  So there are floor(tokens / half) numbers, however many sequences.
+__device__ __forceinline__ int first_state(const Segment &s, int seg) { return s.lo / (seg / 2); }
+// The segment of state number v (s = -1: none).  Row (v + 1) half - 1 is its sequence's: it is not before lo, as
+// (lo / half + 1) half > lo, and at most lo + count half - 1 < lo + len.  Called by whole warps.
+__device__ __forceinline__ Segment find_state(const Packed &q, int seg, int v) {
+    const int half = seg / 2, t = (v + 1) * half - 1;
+    const int i = last_sequence(q, [&](int start, int) { return start <= t; });
+    if (i < 0) return Segment{-1, 0, 0, 0, 0};
+    Segment r = segments_of(q, seg, i);
+    r.k = v - r.lo / half;
+    if (r.count < 2 || t >= r.lo + r.len || r.k < 0 || r.k >= r.count) r.s = -1;
     return r;
 }
 

@@ -670,20 +670,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
         float S[64];                                   // S[h][i][row]
         {
             const float *in = nullptr;
+            const int v0 = first_state(sg, a.seg);
             if (sg.k == 0) {
                 if (last) {
                     const int si = slot_of_start(a.slots, sg.s, a.status);
                     if (si >= 0) in = static_cast<const float *>(a.slots.pool_in) + (size_t)si * a.H * PN;
                 } else {
-                    in = a.ws_state + (size_t)(u + sg.count - 1) * a.H * PN;
+                    in = a.ws_state + (size_t)(v0 + sg.count - 1) * a.H * PN;
                 }
             } else {
-                in = a.ws_state + (size_t)(u - sg.k) * a.H * PN;
+                in = a.ws_state + (size_t)v0 * a.H * PN;
             }
 #pragma unroll
             for (int i = 0; i < 64; ++i) S[i] = in ? in[at + i * 128] : 0.f;
             for (int k = 1; k < sg.k; ++k) {
-                    const size_t v = (size_t)(u - sg.k + k) * a.H;
+                    const size_t v = (size_t)(v0 + k) * a.H;
                     const float d = ex2_ftz(a.ws_decay[v + h]);
                     const float *add = a.ws_state + v * PN + at;
 #pragma unroll
@@ -917,8 +918,8 @@ __global__ void __launch_bounds__(kStThreads, 1) k_ragged_states(const __grid_co
         order_jobs(a, reinterpret_cast<int *>(sm));
         return;
     }
-    const int job = blockIdx.x - 1, pairs = a.H / 2, u = job / pairs, h0 = 2 * (job % pairs), grp = h0 / (a.H / a.G);
-    const Segment sg = find_segment(a.seq, a.seg, u);
+    const int job = blockIdx.x - 1, pairs = a.H / 2, v = job / pairs, h0 = 2 * (job % pairs), grp = h0 / (a.H / a.G);
+    const Segment sg = find_state(a.seq, a.seg, v);
     if (sg.s < 0 || sg.k == sg.count - 1 || (sbase & 1023)) {   // (a misaligned base is reported by k_ragged_tc)
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
@@ -1001,7 +1002,7 @@ __global__ void __launch_bounds__(kStThreads, 1) k_ragged_states(const __grid_co
         if (sg.k == 0) {
             // the sequence's start, kept where its last segment's own state would be (nothing reads that):
             // by the time the scan starts from it the pool may hold the sequence's new state
-            float *keep = a.ws_state + (size_t)(u + sg.count - 1) * a.H * PN + at;
+            float *keep = a.ws_state + (size_t)(v - sg.k + sg.count - 1) * a.H * PN + at;
 #pragma unroll
             for (int i = 0; i < 32; ++i) keep[i * 128] = S[i];
         }
@@ -1067,10 +1068,10 @@ __global__ void __launch_bounds__(kStThreads, 1) k_ragged_states(const __grid_co
             if ((i & 1) && i > 1) ok = add_chunk((i >> 1) - 1);
         }
         if (ok && add_chunk(nc - 1)) {
-            float *out = a.ws_state + (size_t)u * a.H * PN + at;
+            float *out = a.ws_state + (size_t)v * a.H * PN + at;
 #pragma unroll
             for (int i = 0; i < 32; ++i) out[i * 128] = S[i];
-            if (q == 0 && (cg & 1) == 0 && lane == 0) a.ws_decay[(size_t)u * a.H + hs] = total;
+            if (q == 0 && (cg & 1) == 0 && lane == 0) a.ws_decay[(size_t)v * a.H + hs] = total;
         }
     }
     tc_fence_before();
@@ -1118,12 +1119,12 @@ cudaError_t launch_ragged_tc(const RaggedArgs &a, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    if (a.seq.tokens > a.seg) {
+    if (a.states) {
         StMaps sm;
         memset(&sm, 0, sizeof sm);
         if (!map_rows(&sm.x, a.x, T, HP, a.ldx, kHalf) || !map_rows(&sm.b, a.B, T, GN, a.ldB, kHalf)) return cudaErrorInvalidValue;
         if ((e = cudaFuncSetAttribute(k_ragged_states, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStSmem)) != cudaSuccess) return e;
-        cfg.gridDim = dim3(grid + 1);                  // and the CTA that sorts the jobs
+        cfg.gridDim = dim3(a.states * (a.H / 2) + 1);  // and the CTA that sorts the jobs
         cfg.blockDim = dim3(kStThreads);
         cfg.dynamicSmemBytes = kStSmem;
         if ((e = cudaLaunchKernelEx(&cfg, k_ragged_states, sm, a)) != cudaSuccess) return e;

@@ -840,7 +840,7 @@ ssd_status check_step(const ssd_step_shape *s) {
 }
 
 struct RaggedPlan {
-    int seg, units;
+    int seg, units, states;
     size_t state, decay, tables, order, total;     // workspace offsets and size
 };
 
@@ -855,15 +855,20 @@ ssd_status ragged_plan(const ssd_ragged_shape *s, long long tokens, int nseq, Ra
     // 288 / 571, three 302 / 516, four 320 / 554).
     // Others: about four CTAs to an SM.
     const bool tc = s->io == SSD_BF16 && s->headdim == 64 && s->dstate == 128 && (s->nheads / s->ngroups) % 2 == 0;
-    p->seg = tc ? ssd::ragged_segment(tokens, s->nheads / 2, 128, 2 * 148) : ssd::ragged_segment(tokens, s->nheads, 32, 4 * 148);
+    const long long per_seg = tc ? s->nheads / 2 : s->nheads, quant = tc ? 128 : 32, ctas = tc ? 2 * 148 : 4 * 148;
+    p->seg = ssd::ragged_segment(tokens, per_seg, (int)quant, ctas);
     p->units = (int)(tokens / p->seg) + nseq;
     // sequences no longer than a segment need no states between launches
-    const size_t n = tokens > p->seg ? (size_t)p->units * s->nheads : 0;
+    p->states = tokens > p->seg ? (int)(tokens / (p->seg / 2)) : 0;
+    // The sizes go by what the two counts can be at most for this many tokens or fewer (tokens / seg is at most
+    // tokens / quant and ctas / per_seg), so that they never fall as tokens or sequences grow.
+    auto most = [&](long long f) { return tokens <= quant ? 0 : f * tokens / quant < f * ctas / per_seg ? f * tokens / quant : f * ctas / per_seg; };
+    const size_t n = (size_t)most(2) * s->nheads, jobs = tc && tokens > quant ? (size_t)(most(1) + nseq) * (s->nheads / 2) : 0;
     p->state = kStatusBytes;
     p->decay = p->state + round_up(n * s->headdim * s->dstate * sizeof(float));
     p->tables = p->decay + round_up(n * sizeof(float));
     p->order = p->tables + (tc ? round_up((size_t)(tokens / 128 + nseq) * s->nheads * ssd::kRaggedTable * sizeof(float)) : 0);
-    p->total = p->order + (tc ? round_up(n * sizeof(int)) : 0);
+    p->total = p->order + round_up(2 * jobs * sizeof(int));
     return SSD_OK;
 }
 
@@ -942,12 +947,12 @@ ssd_status ssd_scan_ragged(const ssd_ragged_shape *shape, const ssd_packed *seq,
     a.ldx = p->ldx; a.lddt = p->lddt; a.ldB = p->ldB; a.ldC = p->ldC;
     a.A = p->A; a.D = p->D; a.dt_bias = p->dt_bias; a.y = y; a.ldy = ldy;
     a.H = shape->nheads; a.P = shape->headdim; a.N = shape->dstate; a.G = shape->ngroups; a.dir = direction;
-    a.seg = plan.seg; a.units = plan.units;
+    a.seg = plan.seg; a.units = plan.units; a.states = plan.states;
     char *ws = static_cast<char *>(workspace);
     a.ws_state = reinterpret_cast<float *>(ws + plan.state);
     a.ws_decay = reinterpret_cast<float *>(ws + plan.decay);
     a.tables = reinterpret_cast<float *>(ws + plan.tables);
-    a.order = a.seq.tokens > plan.seg ? reinterpret_cast<int *>(ws + plan.order) : nullptr;
+    a.order = plan.states ? reinterpret_cast<int *>(ws + plan.order) : nullptr;
     a.status = static_cast<int *>(workspace);
     a.wait_cycles = wait_cycles_now();
     const bool bf16 = shape->io == SSD_BF16;

@@ -298,7 +298,7 @@ def ssd_conv_bwd(x, w, bias, gy, cu_seqlens=None, direction: int = 1, silu: bool
 
 def ragged_workspace_bytes(tokens: int, nseq: int, nheads: int, headdim: int, dstate: int, ngroups: int = 1,
                            io: torch.dtype = torch.bfloat16) -> int:
-    """Workspace size of ssd_scan_ragged (0: refused)."""
+    """Workspace size of ssd_scan_ragged (0: refused); it never falls as tokens or sequences grow."""
     return int(lib.ssd_ragged_workspace_bytes(_RaggedShape(nheads, headdim, dstate, ngroups, _IO[io]), tokens, nseq))
 
 

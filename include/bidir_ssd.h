@@ -411,7 +411,8 @@ ssd_status ssd_conv_bwd(const ssd_conv_shape *shape, const ssd_packed *seq, cons
  * dt_bias [nheads] may be NULL; all float32.  States: float32
  * [nheads][headdim][dstate] a slot.  headdim in {16,32,64}, dstate in
  * {16,32,64,128}.  y may not overlap an input.  Workspace of
- * ssd_ragged_workspace_bytes, 256-byte aligned, status word zero on entry.
+ * ssd_ragged_workspace_bytes, 256-byte aligned, status word zero on entry; the
+ * size never falls as tokens or sequences grow, so the largest batch's serves all.
  *
  * bf16 with headdim 64, dstate 128, an even number of heads to a group and rows
  * that are multiples of 16 bytes runs on the tensor cores in chunks of 128

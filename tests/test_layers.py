@@ -266,6 +266,27 @@ def test_step_form_is_a_prompt_of_one_token():
     assert torch.allclose(y, want @ v[H * P + N:] + D.double()[:, None] * v[:H * P].reshape(H, P), atol=1e-12)
 
 
+def test_ragged_workspace_does_not_fall_as_a_batch_grows():
+    """A workspace taken for the largest batch serves every smaller one, in tokens and in sequences."""
+    for H, P, N, io in ((64, 64, 128, torch.bfloat16), (2, 64, 128, torch.bfloat16), (600, 64, 128, torch.bfloat16),
+                        (8, 32, 64, torch.float32), (700, 16, 16, torch.float32)):
+        need = lambda T, S: ssd.ragged_workspace_bytes(T, S, H, P, N, 1, io)  # noqa: E731
+        for S in (0, 1, 8, 300):
+            sizes = [need(T, S) for T in (*range(0, 2600, 13), *range(2600, 70000, 701))]
+            assert sizes == sorted(sizes), (H, S)
+        for T in (1, 128, 129, 5000):
+            sizes = [need(T, S) for S in range(0, 400, 7)]
+            assert sizes == sorted(sizes), (H, T)
+
+
+def test_ragged_workspace_of_short_sequences():
+    """States are kept for sequences of two or more segments alone: at most 2 tokens / segment of them, 38 MB here,
+    and 3.3 KB of decay tables a chunk and head."""
+    need = lambda T, S: ssd.ragged_workspace_bytes(T, S, 64, 64, 128)  # noqa: E731
+    for T, S in ((8192, 4096), (16384, 1024), (16384, 256), (3000, 96)):
+        assert need(T, S) <= 39e6 + 64 * (T // 128 + S) * (4 * 840 + 8), (T, S)
+
+
 def test_workspace_queries_agree_with_the_shapes():
     assert ctypes.sizeof(L._Slots) == 40 and ctypes.sizeof(L._Packed) == 16
     assert ssd.ragged_workspace_bytes(16384, 8, 64, 64, 128) > ssd.ragged_workspace_bytes(100, 1, 64, 64, 128) > 0

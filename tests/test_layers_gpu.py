@@ -324,6 +324,36 @@ def test_scan_ragged_many_sequences(ssd, P, N, io, direction):
         _check(pool, last, (6 * n + 40) * U * lastm + 1e-37, "states")
 
 
+@pytest.mark.parametrize("P,N,io,direction", [(64, 128, "bf16", 1), (64, 128, "bf16", -1), (32, 32, "f32", -1)], ids=str)
+def test_scan_ragged_one_workspace_for_all_batches(ssd, P, N, io, direction):
+    """A workspace of the largest batch's size through smaller ones; long sequences among hundreds of short ones (the
+    first, some that begin anywhere in a segment, neighbours, the last), whose states pass between the launches."""
+    dt, H = DT[io], 8
+    g = _gen("one workspace", P, direction)
+    lens = [(1, 0, 2, 3)[i % 4] for i in range(640)]
+    for i, n in ((0, 700), (13, 257), (14, 129), (15, 385), (300, 256), (301, 1000), (639, 131)):
+        lens[i] = n
+    ws = torch.zeros(ssd.ragged_workspace_bytes(6000, 700, H, P, N, 1, dt), dtype=torch.uint8, device="cuda")
+    for lens in (lens, [1185], lens[:16], lens[::-1], [2, 1], [1700, 3]):
+        T, S = sum(lens), len(lens)
+        _, x, B, C, d, A, D, _ = _scan_inputs(g, T, H, P, N, 1, dt, False)
+        x, B, C, d, A, D = (v.contiguous().cuda() for v in (x, B, C, d, A, D))
+        pool = torch.randn(S, H, P, N, generator=g).cuda()
+        start = [pool[i].clone() for i in range(S)]
+        y = ssd.ssd_scan_ragged(x, d, A, B, C, D, cu_seqlens=_cu(lens), direction=direction, state_in=pool, state_out=pool,
+                                workspace=ws)
+        ssd.workspace_status(ws)
+        ref, ym, last, lastm = ol.scan(x, d, A, B, C, D, lens, None, direction, start)
+        ref, ym, last, lastm = ref.cpu(), ym.cpu(), torch.stack(list(last)).cpu(), torch.stack(list(lastm)).cpu()
+        n = max(lens)
+        if io == "bf16":
+            _check(y, ref, _tc_y(n, N, ref, ym), "y")
+            _check(pool, last, _tc_s(n, last, lastm), "states")
+        else:
+            _check(y, ref, HALF[dt] * ref.abs() + (1 + HALF[dt]) * (6 * n + 2 * N + 40) * U * ym + 1e-37, "y")
+            _check(pool, last, (6 * n + 40) * U * lastm + 1e-37, "states")
+
+
 def test_scan_ragged_neighbours_do_not_leak(ssd):
     """NaN and infinity in one sequence (and behind the last) leave the others bit for bit, states too."""
     g = _gen("leak")
