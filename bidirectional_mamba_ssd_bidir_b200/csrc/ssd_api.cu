@@ -710,7 +710,9 @@ ssd_status check_packed(const ssd_packed *q, ssd::Packed *out) {
     return SSD_OK;
 }
 
-ssd_status check_slots(const ssd_slots *q, int nseq, size_t align, ssd::Slots *out) {
+// `slot`: bytes of one state.  Two pools that share a part of their memory are refused: the kernels tell a slot that
+// one sequence writes and another starts from by its number, in one pool.
+ssd_status check_slots(const ssd_slots *q, int nseq, size_t align, size_t slot, ssd::Slots *out) {
     *out = ssd::Slots{};
     if (!q) return SSD_OK;
     if (!aligned(q->pool_in, align) || !aligned(q->pool_out, align) || !aligned(q->slots_in, 4) || !aligned(q->slots_out, 4))
@@ -718,6 +720,9 @@ ssd_status check_slots(const ssd_slots *q, int nseq, size_t align, ssd::Slots *o
     if (q->n_in < 0 || q->n_out < 0) return fail(SSD_ERR_INVALID_ARG, "negative slot count");
     if ((q->pool_in && !q->slots_in && q->n_in < nseq) || (q->pool_out && !q->slots_out && q->n_out < nseq))
         return fail(SSD_ERR_INVALID_ARG, "a state pool without slot indices needs one slot per sequence (%d)", nseq);
+    const uintptr_t in = reinterpret_cast<uintptr_t>(q->pool_in), out_ = reinterpret_cast<uintptr_t>(q->pool_out);
+    if (in && out_ && in != out_ && in < out_ + q->n_out * slot && out_ < in + q->n_in * slot)
+        return fail(SSD_ERR_INVALID_ARG, "pool_in and pool_out overlap in part (one pool, or two apart)");
     out->pool_in = q->pool_in; out->pool_out = q->pool_out;
     out->in = q->slots_in; out->out = q->slots_out;
     out->n_in = q->n_in; out->n_out = q->n_out;
@@ -758,7 +763,7 @@ ssd_status ssd_conv(const ssd_conv_shape *shape, const ssd_packed *seq, const vo
     g_err.clear();
     ssd::ConvArgs a;
     ssd_status st = conv_args(shape, seq, &a);
-    if (st != SSD_OK || (st = check_slots(state, a.seq.nseq, io_bytes(shape->io), &a.slots)) != SSD_OK) return st;
+    if (st != SSD_OK || (st = check_slots(state, a.seq.nseq, io_bytes(shape->io), (size_t)(a.K - 1) * a.C * io_bytes(shape->io), &a.slots)) != SSD_OK) return st;
     if ((st = check_status_area(workspace, workspace_bytes)) != SSD_OK) return st;
     if (a.seq.nseq == 0) return SSD_OK;
     const size_t es = io_bytes(shape->io);
@@ -929,7 +934,8 @@ ssd_status ssd_scan_ragged(const ssd_ragged_shape *shape, const ssd_packed *seq,
     ssd_status st = check_packed(seq, &a.seq);
     if (st != SSD_OK || (st = ragged_plan(shape, a.seq.tokens, a.seq.nseq, &plan)) != SSD_OK) return st;
     if (direction != 1 && direction != -1) return fail(SSD_ERR_INVALID_ARG, "direction must be +1 or -1");
-    if ((st = check_slots(state, a.seq.nseq, 4, &a.slots)) != SSD_OK) return st;
+    if ((st = check_slots(state, a.seq.nseq, 4, sizeof(float) * shape->nheads * shape->headdim * shape->dstate, &a.slots)) != SSD_OK)
+        return st;
     if (!p) return fail(SSD_ERR_INVALID_ARG, "params is NULL");
     if (a.seq.nseq == 0) return SSD_OK;
     const size_t es = io_bytes(shape->io);

@@ -356,8 +356,8 @@ typedef struct {
  * pool_in (a negative index, or pool_in NULL: from zero) and leaves the state
  * after its last token in slot slots_out[i] of pool_out (negative, or pool_out
  * NULL: not stored).  slots_in / slots_out are DEVICE arrays of nseq ints; NULL
- * means slot i.  pool_in and pool_out may be the same buffer, and a sequence
- * may end in the slot it started from; no other sequence of the call may start
+ * means slot i.  pool_in and pool_out may be the same buffer (overlapping in
+ * part, they are refused), and a sequence may end in the slot it started from; no other sequence of the call may start
  * from a slot that one of them writes.  An empty sequence passes its state
  * on.  A slot index past n_in / n_out counts as no slot, and a slot that
  * another sequence of the call uses too is not written (two that would write

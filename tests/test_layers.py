@@ -132,6 +132,22 @@ def test_ffn_refusals():
     assert back(gwi=None) == INVALID and back(gwo=GOOD + 4) == INVALID and back(wsb=bwd - 1) == INVALID
 
 
+def test_pools_that_overlap_in_part_are_refused():
+    """A slot that one sequence writes and another reads is told by its number, which overlapping pools would hide."""
+    slot = 3 * 8 * 2                                                 # ssd_conv's state here, bytes
+    for other in (GOOD + slot, GOOD + 3 * slot + 2, GOOD - 3 * slot, GOOD + 4 * slot - 2):
+        assert _conv(slots=(GOOD, other, None, None, 4, 4)) == INVALID and "overlap" in _err()
+    need = lib.ssd_ragged_workspace_bytes(L._RaggedShape(4, 32, 64, 2, 1), 100, 3)
+    slot = 4 * 32 * 64 * 4
+    for other in (GOOD + slot, GOOD - slot, GOOD + 3 * slot - 4):
+        p = L._RaggedParams(GOOD, GOOD, GOOD, GOOD, 128, 4, 128, 128, GOOD, None, None)
+        assert lib.ssd_scan_ragged(L._RaggedShape(4, 32, 64, 2, 1), L._Packed(GOOD, 3, 100), p, 1,
+                                   L._Slots(GOOD, other, None, None, 3, 3), GOOD, 128, GOOD, need, None) == INVALID and "overlap" in _err()
+    # the same pool, and two that touch, go on to the checks behind
+    for other in (GOOD, GOOD + 4 * 48, GOOD - 4 * 48):
+        assert _conv(slots=(GOOD, other, None, None, 4, 4), x=None) == INVALID and "overlap" not in _err()
+
+
 # ---------------------------------------------------------------- refusals of the binding
 
 def test_binding_refuses_cpu_tensors():
