@@ -238,6 +238,17 @@ def _no_overlap(out, yp, ldy, width, rows, *ins):
         raise ValueError("out overlaps an input")
 
 
+def _apart(out, *states):
+    """Refuse an ``out`` laid over a state that the call reads or writes."""
+    for t in states:
+        if t is None or t.untyped_storage().data_ptr() != out.untyped_storage().data_ptr() or t.numel() == 0 or out.numel() == 0:
+            continue
+        last = sum((n - 1) * s for n, s in zip(out.shape, out.stride()))
+        if out.data_ptr() < t.data_ptr() + t.numel() * t.element_size() and \
+                t.data_ptr() < out.data_ptr() + (last + 1) * out.element_size():
+            raise ValueError("out overlaps a state")
+
+
 def _conv_bwd_bytes(C, K, tokens):
     return lib.ssd_conv_bwd_workspace_bytes(_ConvShape(C, K, 1, 1, 0), tokens)
 
@@ -269,6 +280,7 @@ def ssd_conv(x, w, bias=None, cu_seqlens=None, direction: int = 1, silu: bool = 
     yp, ldy = (y.data_ptr(), C) if out is None else _rows("out", y, batched, lead, (C,), x.dtype, dev)
     if out is not None:
         _no_overlap(out, yp, ldy, C, seq.tokens, (x, xp, ldx, C))
+        _apart(out, state_in, state_out)
     slots = _slots(state_in, state_out, slots_in, slots_out, (K - 1, C), x.dtype, seq.nseq, dev)
     ws, wp, wn = (None, None, 0) if workspace is None else _scratch(workspace, 256, x)
     _call(dev, lib.ssd_conv, _ConvShape(C, K, int(direction), int(silu), io), seq, xp, ldx, _f32("w", w, (C, K), dev),
@@ -325,6 +337,7 @@ def ssd_scan_ragged(x, dt, A, B, C, D=None, cu_seqlens=None, dt_bias=None, direc
     if out is not None:
         _no_overlap(out, yp, ldy, H * P, seq.tokens, (x, xp, ldx, H * P), (dt, dp, ldd, H), (B, bp, ldb, G * N),
                     (C, cp, ldc, G * N))
+        _apart(out, state_in, state_out)
     slots = _slots(state_in, state_out, slots_in, slots_out, (H, P, N), torch.float32, seq.nseq, dev)
     shape = _RaggedShape(H, P, N, G, io)
     prm = _RaggedParams(xp, dp, bp, cp, ldx, ldd, ldb, ldc, _f32("A", A, (H,), dev), _f32("D", D, (H,), dev),
@@ -367,6 +380,7 @@ def mamba2_step(xBC, dt, conv_w, conv_b, dt_bias, A, D, conv_state, ssm_state, s
     yp, ldy = (y.data_ptr(), H * P) if out is None else _rows("out", y, False, lead, (H, P), dtype, dev)
     if out is not None:
         _no_overlap(out, yp, ldy, H * P, R, (xBC, xp, ldx, Cc), (dt, dp, ldd, H))
+        _apart(out, conv_state, ssm_state)
     shape = _StepShape(R, n, H, P, N, ngroups, K, io)
     ws, wp, wn = _scratch(workspace, _bytes(_step_bytes, "step", R, H, P, N, ngroups, K), xBC)
     _call(dev, lib.mamba2_step, shape, xp, ldx, dp, ldd, _f32("conv_w", conv_w, (Cc, K), dev), _f32("conv_b", conv_b, (Cc,), dev),

@@ -203,6 +203,17 @@ def test_binding_overlap_check():
             check(x, y)
 
 
+def test_binding_refuses_an_out_over_a_state():
+    t = torch.zeros(400)
+    pool, out = t[:96].view(4, 3, 8), t[96:].view(-1, 16)[:, :8]
+    L._apart(out, pool, None)
+    L._apart(out, torch.zeros(4, 3, 8))
+    L._apart(t[0:0].view(0, 8), pool)
+    for o in (t[95:200], t[40:140].view(-1, 20)[:, :8], pool[1], t):
+        with pytest.raises(ValueError, match="overlaps a state"):
+            L._apart(o, None, pool)
+
+
 # ---------------------------------------------------------------- pins of the float64 forms
 
 @pytest.mark.parametrize("direction", [1, -1])

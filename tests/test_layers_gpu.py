@@ -573,6 +573,21 @@ def test_a_slot_another_sequence_starts_from_is_kept(ssd):
               torch.randn(4, 2, P, N, generator=g).cuda(), ssd.ragged_workspace_bytes(T, 2, 2, P, N, 1, dt))
 
 
+def test_an_out_over_a_state_is_refused(ssd):
+    """Refused before anything is launched: the outputs' buffer is a part of the state pool."""
+    z = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    conv, ssm = z(2, 3, 8), z(2, 2, 16, 16)
+    with pytest.raises(ValueError, match="overlaps a state"):
+        ssd.ssd_conv(z(6, 8), z(8, 4), cu_seqlens=_cu([6]), state_out=conv, out=conv.view(6, 8))
+    with pytest.raises(ValueError, match="overlaps a state"):
+        ssd.ssd_scan_ragged(z(4, 2, 16), z(4, 2), z(2), z(4, 1, 16), z(4, 1, 16), cu_seqlens=_cu([4]), state_in=ssm,
+                            out=ssm.view(-1)[:128].view(4, 2, 16))
+    conv = z(2, 3, 64)
+    for over in (ssm.view(-1)[64:128], conv.view(-1)[:64]):
+        with pytest.raises(ValueError, match="overlaps a state"):
+            ssd.mamba2_step(z(2, 64), z(2, 2), z(64, 4), None, None, z(2), None, conv, ssm, out=over.view(2, 2, 16))
+
+
 def test_graph_replays_follow_new_inputs(ssd):
     """A captured decoding step (padded batch, slots in a device tensor) replayed on new contents, and on a
     side stream."""
