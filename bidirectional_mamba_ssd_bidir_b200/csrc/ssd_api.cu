@@ -980,6 +980,7 @@ ssd_status ffn_checks(const ssd_ffn_shape *s) {
         return fail(SSD_ERR_INVALID_ARG, "unknown activation %d", (int)s->activation);
     if (s->d_model % 8 != 0 || s->d_ff % 8 != 0)
         return fail(SSD_ERR_UNSUPPORTED, "feed-forward block needs d_model and d_ff multiples of 8");
+    if (s->tokens > 0x7fff0000) return fail(SSD_ERR_UNSUPPORTED, "too many tokens");      // (rounded up to tiles in ints)
     if (s->d_ff > (1 << 28) || s->d_model > (1 << 28)) return fail(SSD_ERR_UNSUPPORTED, "d_model and d_ff up to 2^28");
     return SSD_OK;
 }

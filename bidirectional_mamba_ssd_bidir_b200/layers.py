@@ -97,6 +97,12 @@ def _io_of(t) -> int:
     return io
 
 
+def _sizes(*ns):
+    """Refuse sizes past the C entry points' ints (ctypes would pass them on modulo 2^32)."""
+    if max(ns) > 0x7fffffff:
+        raise ValueError(f"sizes {ns}: at most 2^31 - 1 tokens, sequences, channels or slots")
+
+
 def _cuda(name, t):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -170,12 +176,14 @@ def _packed(x, tail_dims, cu_seqlens, dev):
         if len(shape) != tail_dims + 2:
             raise ValueError("without cu_seqlens the tensors need a batch and a token dimension")
         b, n = shape[:2]
+        _sizes(b, b * n)
         return _Packed(None, b, b * n), True, shape[:2]
     if len(shape) != tail_dims + 1:
         raise ValueError("with cu_seqlens the tensors have one token dimension and no batch dimension")
     n = cu_seqlens.numel()
     if n < 1:
         raise ValueError("cu_seqlens must be int32 of shape (nseq + 1,)")
+    _sizes(n, shape[0])
     return _Packed(_i32("cu_seqlens", cu_seqlens, n, dev), n - 1, shape[0]), False, shape[:1]
 
 
@@ -185,6 +193,7 @@ def _pool(name, t, tail, dtype, dev):
     shape = t.shape
     if t.dtype is not dtype or shape[1:] != tail or len(shape) != len(tail) + 1 or t.get_device() != dev.index or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} of shape (slots, {', '.join(map(str, tail))}) on {dev}")
+    _sizes(shape[0])
     return t.data_ptr(), shape[0]
 
 
@@ -274,6 +283,7 @@ def ssd_conv(x, w, bias=None, cu_seqlens=None, direction: int = 1, silu: bool = 
     if w.dim() != 2:
         raise ValueError("w must be float32 [channels, width]")
     C, K = w.shape
+    _sizes(C, K)
     seq, batched, lead = _packed(x, 1, cu_seqlens, dev)
     xp, ldx = _rows("x", x, batched, lead, (C,), x.dtype, dev)
     y = x.new_empty(x.shape) if out is None else out
@@ -295,6 +305,7 @@ def ssd_conv_bwd(x, w, bias, gy, cu_seqlens=None, direction: int = 1, silu: bool
     if w.dim() != 2:
         raise ValueError("w must be float32 [channels, width]")
     C, K = w.shape
+    _sizes(C, K)
     seq, batched, lead = _packed(x, 1, cu_seqlens, dev)
     xp, ldx = _rows("x", x, batched, lead, (C,), x.dtype, dev)
     gp, ldg = _rows("gy", gy, batched, lead, (C,), x.dtype, dev)
@@ -311,6 +322,7 @@ def ssd_conv_bwd(x, w, bias, gy, cu_seqlens=None, direction: int = 1, silu: bool
 def ragged_workspace_bytes(tokens: int, nseq: int, nheads: int, headdim: int, dstate: int, ngroups: int = 1,
                            io: torch.dtype = torch.bfloat16) -> int:
     """Workspace size of ssd_scan_ragged (0: refused); it never falls as tokens or sequences grow."""
+    _sizes(tokens, nseq)
     return int(lib.ssd_ragged_workspace_bytes(_RaggedShape(nheads, headdim, dstate, ngroups, _IO[io]), tokens, nseq))
 
 
@@ -349,6 +361,7 @@ def ssd_scan_ragged(x, dt, A, B, C, D=None, cu_seqlens=None, dt_bias=None, direc
 
 def step_workspace_bytes(rows: int, nheads: int, headdim: int, dstate: int, ngroups: int = 1, d_conv: int = 4) -> int:
     """Workspace size of mamba2_step (0: refused)."""
+    _sizes(rows)
     return int(lib.ssd_step_workspace_bytes(_StepShape(rows, rows, nheads, headdim, dstate, ngroups, d_conv, 0)))
 
 
@@ -365,6 +378,7 @@ def mamba2_step(xBC, dt, conv_w, conv_b, dt_bias, A, D, conv_state, ssm_state, s
     if xBC.dim() != 2 or ssm_state.dim() != 4 or conv_w.dim() != 2:
         raise ValueError("xBC must be [rows, channels], ssm_state [slots, nheads, headdim, dstate], conv_w [channels, d_conv]")
     R, Cc = xBC.shape
+    _sizes(R, Cc)
     n, H, P, N = ssm_state.shape
     K = conv_w.shape[1]
     if Cc != H * P + 2 * ngroups * N:
@@ -398,7 +412,9 @@ def _ffn_shape(u, W_in, W_out, activation, dev):
     if W_in.dim() != 2 or W_out.dim() != 2 or u.dim() < 1:
         raise ValueError("u must be [..., d_model], W_in [2 d_ff, d_model], W_out [d_model, d_ff]")
     D, F = W_out.shape
-    return _FfnShape(u.numel() // D if D else 0, D, F, _ACT[activation])
+    T = u.numel() // D if D else 0
+    _sizes(T, D, F)
+    return _FfnShape(T, D, F, _ACT[activation])
 
 
 def _bf16(name, t, shape, dev):
@@ -409,11 +425,13 @@ def _bf16(name, t, shape, dev):
 
 def ffn_workspace_bytes(tokens: int, d_model: int, d_ff: int) -> int:
     """Workspace size of ffn_block (0: refused)."""
+    _sizes(tokens, d_model, d_ff)
     return int(lib.ssd_ffn_workspace_bytes(_FfnShape(tokens, d_model, d_ff, 0)))
 
 
 def ffn_bwd_workspace_bytes(tokens: int, d_model: int, d_ff: int) -> int:
     """Workspace size of ffn_block_bwd (0: refused)."""
+    _sizes(tokens, d_model, d_ff)
     return int(lib.ssd_ffn_bwd_workspace_bytes(_FfnShape(tokens, d_model, d_ff, 0)))
 
 

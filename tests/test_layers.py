@@ -188,6 +188,23 @@ def test_binding_row_checks():
         checked(torch.zeros(2, 4, 8)[:, :3], (8,), b=True)
 
 
+def test_binding_refuses_sizes_past_an_int():
+    """2^32 + 5 tokens would reach the C entry points as 5."""
+    big, cu = 2 ** 32 + 5, torch.zeros(3, dtype=torch.int32)
+    one, w = torch.zeros(1, 1), torch.zeros(8, 8)
+    for call in (lambda: L._packed(one.expand(big, 8), 1, cu, _Dev), lambda: L._packed(one.expand(2 ** 16, 2 ** 16)[:, :, None], 1, None, _Dev),
+                 lambda: L._packed(torch.zeros(1, 1, 1).expand(big, 0, 8), 1, None, _Dev),
+                 lambda: L._ffn_shape(one.expand(big, 8), w, w, "silu", _Dev),
+                 lambda: ssd.ragged_workspace_bytes(big, 1, 2, 64, 128), lambda: ssd.ragged_workspace_bytes(1, big, 2, 64, 128),
+                 lambda: ssd.step_workspace_bytes(big, 2, 64, 128), lambda: ssd.ffn_workspace_bytes(big, 8, 8),
+                 lambda: ssd.ffn_bwd_workspace_bytes(8, big, 8)):
+        with pytest.raises(ValueError, match="sizes"):
+            call()
+    assert L._packed(one.expand(2 ** 31 - 1, 8), 1, cu, _Dev)[0].tokens == 2 ** 31 - 1
+    # (the entry points round the tokens up to tiles in ints)
+    assert ssd.ffn_workspace_bytes(2 ** 31 - 1, 8, 8) == ssd.ffn_bwd_workspace_bytes(2 ** 31 - 1, 8, 8) == 0
+
+
 def test_binding_overlap_check():
     t = torch.zeros(6, 40)
     a, b, c = t[:, 0:16], t[:, 16:32], t[:, 10:26]
