@@ -111,6 +111,107 @@ def test_backward(ssd, T, D, F, act):
     _check(got["W_out"], ref, tol(ref.t(), h.t(), hoff.t(), gy, T).t(), "W_out")
 
 
+# ---------------------------------------------------------------- several tiles to a CTA group
+
+def _within(got, ref, tol, what):
+    """_check on the GPU."""
+    got = got.double()
+    assert bool(torch.isfinite(got).all()), what
+    over = ((got - ref).abs() - tol).max()
+    assert bool(over <= 0), f"{what}: off by {(got - ref).abs().max():.3e}, over its bound by {over:.3e}"
+
+
+def _tiles(M, N, width, pair):
+    """Tiles of the persistent kernel for a product [M][N] (128 or 256 rows, `width` columns), per CTA or pair of them."""
+    groups = torch.cuda.get_device_properties(0).multi_processor_count // pair
+    return -(-M // (128 * pair)) * -(-N // width) / groups
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_many_tiles_a_group(ssd, act):
+    """Accumulators, staging boxes and the load ring handed on from tile to tile, in each launch of the persistent
+    kernel: three tiles or more to every CTA pair, ragged in all directions.  Bounds as above; float64 on the GPU."""
+    T, D, F = 4100, 3592, 3720
+    for M, N, width in ((T, F, 128), (T, D, 256), (T, F, 256), (T, D, 256), (2 * F, D, 256), (D, F, 256)):
+        assert _tiles(M, N, width, 2) >= 3
+    bf = _inputs(T, D, F, 3)
+    u16, wi16, wo16, gy16 = (t.cuda() for t in bf)
+    ws = torch.zeros(ssd.ffn_workspace_bytes(T, D, F), dtype=torch.uint8, device="cuda")
+    out, gu16 = ssd.ffn_block(u16, wi16, wo16, activation=act, save=True, workspace=ws)
+    ssd.workspace_status(ws)
+    assert torch.equal(out, ssd.ffn_block(u16, wi16, wo16, activation=act))
+    u, wi, wo, gy = (t.double() for t in (u16, wi16, wo16, gy16))
+    pre, mag = u @ wi.t(), u.abs() @ wi.abs().t()
+    _within(gu16, pre, R * pre.abs() + (1 + R) * (D + 8) * U * mag + 1e-30, "gu")
+    g, p = pre[:, :F], pre[:, F:]
+    a, _ = _act(act, g)
+    h, e = a * p, (D + 8) * U
+    eh = e * (1.2 * mag[:, :F] * p.abs() + a.abs() * mag[:, F:] + 1.2 * e * mag[:, :F] * mag[:, F:])
+    eh = eh + (U * 8 * g.abs() * p.abs() if act == "gelu" else 0)
+    tol = R * (h @ wo.t()).abs() + (1 + R) * ((R + 2.0 ** -19) * h.abs() + eh + F * U * h.abs()) @ wo.abs().t() + 1e-30
+    _within(out, h @ wo.t(), tol, "out")
+    del pre, mag, eh, tol
+
+    ws = torch.zeros(ssd.ffn_bwd_workspace_bytes(T, D, F), dtype=torch.uint8, device="cuda")
+    got = ssd.ffn_block_bwd(u16, wi16, wo16, gu16, gy16, activation=act, workspace=ws)
+    ssd.workspace_status(ws)
+    g, p = gu16.double().chunk(2, 1)
+    a, da = _act(act, g)
+    gh, ghm = gy @ wo, (gy.abs() @ wo.abs()) * (D * U)
+    ggu = torch.cat([gh * p * da, gh * a], 1)
+    slack = torch.cat([ghm * (p * da).abs(), ghm * a.abs()], 1)
+    if act == "gelu":
+        slack += torch.cat([gh.abs() * p.abs() * 8 * U * (1 + g.abs()), gh.abs() * g.abs() * 8 * U], 1)
+    else:
+        slack += torch.cat([gh.abs() * p.abs() * 16 * U * (1 + g.abs()), 0 * gh], 1)
+    off = (R + 2.0 ** -18) * ggu.abs() + (1 + R) * slack
+    h = a * p
+    hoff = (R + 2.0 ** -18) * h.abs() + (8 * U * (g * p).abs() if act == "gelu" else 0)
+
+    def tol(ref, A, Aoff, B, K):
+        return R * ref.abs() + (1 + R) * (Aoff @ B.abs() + K * U * (A.abs() @ B.abs())) + 1e-30
+
+    ref = ggu @ wi
+    _within(got["u"], ref, tol(ref, ggu, off, wi, 2 * F), "u")
+    ref = ggu.t() @ u
+    _within(got["W_in"], ref, tol(ref, ggu.t(), off.t(), u, T), "W_in")
+    ref = (h.t() @ gy).t()
+    _within(got["W_out"], ref, tol(ref.t(), h.t(), hoff.t(), gy, T).t(), "W_out")
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_many_tiles_a_cta(ssd, act):
+    """The same for the single-CTA form of the activation's gradient (up to 128 tokens): its outputs are operands of
+    the three products, so a tile that is lost or mixed up shows in all of them."""
+    T, D, F = 100, 16, 113800
+    assert _tiles(T, F, 256, 1) >= 3
+    u16, wi16, wo16, gy16 = (t.cuda() for t in _inputs(T, D, F, 4))
+    gu16 = (u16.float() @ wi16.float().t()).to(torch.bfloat16)
+    got = ssd.ffn_block_bwd(u16, wi16, wo16, gu16, gy16, activation=act)
+    u, wi, wo, gy = (t.double() for t in (u16, wi16, wo16, gy16))
+    g, p = gu16.double().chunk(2, 1)
+    a, da = _act(act, g)
+    gh, ghm = gy @ wo, (gy.abs() @ wo.abs()) * (D * U)
+    ggu, h = torch.cat([gh * p * da, gh * a], 1), a * p
+    # (1 + |g|) 16 u of the factors covers both activations' derivative
+    off = (R + 2.0 ** -18) * ggu.abs() + (1 + R) * torch.cat([ghm * (p * da).abs() + gh.abs() * p.abs() * 16 * U * (1 + g.abs()),
+                                                            ghm * a.abs() + gh.abs() * g.abs() * 8 * U], 1)
+    hoff = (R + 2.0 ** -18) * h.abs() + 8 * U * (g * p).abs()
+    for name, A, Aoff, B, K in (("u", ggu, off, wi, 2 * F), ("W_in", ggu.t(), off.t(), u, T), ("W_out", h.t(), hoff.t(), gy, T)):
+        ref = A @ B
+        tol = R * ref.abs() + (1 + R) * (Aoff @ B.abs() + K * U * (A.abs() @ B.abs())) + 1e-30
+        _within(got[name] if name != "W_out" else got[name].t(), ref, tol, name)
+
+
+def test_repeats_itself(ssd):
+    """Equal inputs give equal bits: the split sums are added in a fixed order."""
+    for T, D, F in ((3, 512, 1024), (300, 264, 520), (2100, 136, 264)):
+        u, wi, wo, gy = (t.cuda() for t in _inputs(T, D, F, 6))
+        (a, gu), (b, _) = (ssd.ffn_block(u, wi, wo, save=True) for _ in range(2))
+        g, h = (ssd.ffn_block_bwd(u, wi, wo, gu, gy) for _ in range(2))
+        assert torch.equal(a, b) and all(torch.equal(g[k], h[k]) for k in g)
+
+
 def test_gradient_matches_differences(ssd):
     """The gradients against central differences of the block itself, in float64 on the same inputs."""
     T, D, F = 9, 16, 24
