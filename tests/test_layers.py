@@ -293,6 +293,26 @@ def test_scan_form_pieces_and_softplus():
     assert bool((s[1] == 0).all())                                   # an empty sequence: its start state
 
 
+def test_three_terms_of_bf16_and_not_two_carry_a_float32_state():
+    """What a state built from w x in two or three bf16 terms is off by, as a root mean square: the GPU tests'
+    bound for states, 1e-6, lies between the two."""
+    g = torch.Generator().manual_seed(8)
+    T, P, N = 512, 64, 128
+    x, B = (torch.randn(*s, generator=g).to(torch.bfloat16).double() for s in ((T, P), (T, N)))
+    w = torch.exp(-torch.rand(T, generator=g)).mul(0.05).double()     # float32 weights
+    wx = w[:, None] * x
+    exact = wx.t() @ B
+    off = []
+    for terms in (2, 3):
+        left, s = wx.float(), torch.zeros(P, N, dtype=torch.float64)
+        for _ in range(terms):
+            t = left.to(torch.bfloat16)
+            s += t.double().t() @ B
+            left = left - t.float()
+        off.append(float((s - exact).norm() / exact.norm()))
+    assert off[0] > 1.2e-6 and off[1] < 1e-7, off
+
+
 def test_step_form_is_a_prompt_of_one_token():
     g = torch.Generator().manual_seed(7)
     H, P, N, K = 2, 4, 3, 3

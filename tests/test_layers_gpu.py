@@ -296,6 +296,48 @@ def test_scan_ragged_tensor_core_long(ssd, lens, H, G, direction, carry, steep):
     for i in range(S):
         _check(pool[i], last[i].cpu(), _tc_s(lens[i], last[i].cpu(), lastm[i].cpu()), f"state {i}")
 
+
+# The states of gently decaying inputs.  With u = 2^-24 and decays of at most 1 (as log2) a chunk: w is one product, one
+# ex2 within 4 u and an exponent off by a few u, its product with x and the three terms another 2 u; a chunk's sum of
+# 24 steps of the tensor core rounds to some sqrt(24) u in the root mean square, a chunk's decay to 5 u, and two or
+# three chunks are remembered: in all some 16 u = 1e-6 relative, as a root mean square over a head's state.  Two
+# bf16 terms of w x instead of three would be off by more (tests/test_layers.py measures it on the CPU).
+STATE_RMS = 1e-6
+
+
+@pytest.mark.parametrize("lens,H,direction", [([128], 4, 1), ([900], 64, -1), ([3000], 64, 1), ([1500, 77, 811], 64, -1)], ids=str)
+@pytest.mark.parametrize("beside", [0.01, 90.0], ids=["short", "long"])
+def test_scan_ragged_tensor_core_states_are_float32(ssd, lens, H, direction, beside):
+    """Root mean square error of each gentle head's state.  The other head of a pair decays gently too, or by so much
+    that both take the long form; one segment or several, so both kernels that form states are behind it."""
+    P, N, T, S = 64, 128, sum(lens), len(lens)
+    g = _gen("rms", tuple(lens))
+    _, x, B, C, d, _, D, _ = _scan_inputs(g, T, H, P, N, 1, torch.bfloat16, False)
+    A = torch.rand(H, generator=g) * -0.04 - 0.01
+    A[1::2] = -beside
+    x, B, C, d, A, D = (v.contiguous().cuda() for v in (x, B, C, d, A, D))
+    pool = torch.empty(S, H, P, N, device="cuda")
+    decay = (d.double() * A.double()).abs() / 0.6931
+    assert float(decay[:, 0::2].mean()) * 128 < 1 and (beside < 1 or float(decay[:, 1].mean()) * 128 > 300)
+    ssd.ssd_scan_ragged(x, d, A, B, C, D, cu_seqlens=_cu(lens), direction=direction, state_out=pool)
+    _, _, last, _ = ol.scan(x, d, A, B, C, D, lens, None, direction)
+    for i in range(S):
+        rms = ((pool[i].double() - last[i]).norm(dim=(1, 2)) / last[i].norm(dim=(1, 2)))[0::2]
+        assert float(rms.max()) <= STATE_RMS, (i, rms.max())
+
+
+def test_scan_ragged_repeats_itself(ssd):
+    """Equal inputs give equal bits, whatever order the jobs are taken in."""
+    g = _gen("repeat scan")
+    for lens, H, P, N, dt in (([2000, 3, 700], 64, 64, 128, torch.bfloat16), ([300, 20], 4, 32, 64, torch.float32)):
+        T, S = sum(lens), len(lens)
+        _, x, B, C, d, A, D, _ = _scan_inputs(g, T, H, P, N, 1, dt, False)
+        x, B, C, d, A, D = (v.contiguous().cuda() for v in (x, B, C, d, A, D))
+        states = [torch.zeros(S, H, P, N, device="cuda") for _ in range(4)]
+        ys = [ssd.ssd_scan_ragged(x, d, A, B, C, D, cu_seqlens=_cu(lens), state_out=s) for s in states]
+        assert all(torch.equal(ys[0], y) for y in ys) and all(torch.equal(states[0], s) for s in states)
+
+
 @pytest.mark.parametrize("P,N,io,direction", [(64, 128, "bf16", 1), (64, 128, "bf16", -1), (16, 16, "f32", 1)], ids=str)
 def test_scan_ragged_many_sequences(ssd, P, N, io, direction):
     """More sequences than are looked at together, most of them empty or a token long, some of several segments."""
