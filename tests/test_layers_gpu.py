@@ -487,6 +487,33 @@ def test_step(ssd, R, n, H, P, N, G, K, io):
         assert torch.equal(ssm[s], a["ssm_state"][s])
 
 
+@pytest.mark.parametrize("R,n,H,P,N,G,K,io", [s for s in STEP if s[-1] == "f32"], ids=str)
+def test_step_rounds_nothing_in_between(ssd, R, n, H, P, N, G, K, io):
+    """float32: element by element, so that a rounding to fewer bits anywhere between the inputs and y would show.
+    The convolution's output v is within e = (2 (K + 1) M + (8 + 2 |s|) |v|) u, and with S' the new state
+    |dS| <= 40 u |S| + d (e_x |B| + |x| e_B),  |dy| <= (2 N + 60) u Y + sum_n (|dS| |C| + |S'| e_C) + |D| e_x."""
+    g = _gen("step exact", R, H, P, N, K)
+    a = _step_inputs(g, R, n, H, P, N, G, K, torch.float32)
+    slots = torch.randperm(n, generator=g)[:R].to(torch.int32)
+    d = {k: v.cuda() for k, v in a.items()}
+    y = ssd.mamba2_step(**d, slots=slots.cuda(), ngroups=G).cpu()
+    ssm = d["ssm_state"].cpu()
+    for r, s in enumerate(slots.tolist()):
+        yr, ym, _, S, Sm = ol.step(a["xBC"][r], a["dt"][r], a["conv_w"], a["conv_b"], a["dt_bias"], a["A"], a["D"],
+                                   a["conv_state"][s], a["ssm_state"][s], G)
+        v, pre, mag, _ = ol.conv(a["xBC"][r:r + 1], a["conv_w"], a["conv_b"], [1], 1, True, [a["conv_state"][s]])
+        e = ((2 * (K + 1) * mag + (8 + 2 * pre.abs()) * v.abs()) * U)[0]
+        heads = lambda t: (t[:H * P].reshape(H, P), t[H * P:H * P + G * N].reshape(G, N).repeat_interleave(H // G, 0),  # noqa: E731
+                           t[H * P + G * N:].reshape(G, N).repeat_interleave(H // G, 0))
+        (x, B, C), (ex, eB, eC) = heads(v[0].abs()), heads(e)
+        dt = ol.softplus(a["dt"][r].double() + a["dt_bias"].double())[:, None, None]
+        eS = 40 * U * Sm + 1.01 * dt * (ex[:, :, None] * B[:, None] + x[:, :, None] * eB[:, None])
+        _check(ssm[s], S, eS, "state")
+        ey = (2 * N + 60) * U * ym + 1.01 * ((eS * C[:, None]).sum(-1) + (S.abs() * eC[:, None]).sum(-1) + a["D"].double().abs()[:, None] * ex)
+        assert float((ey / ym).median()) < 2.0 ** -14           # float32's order, far from bf16's 2^-8
+        _check(y[r], yr, ey, "y")
+
+
 def test_step_strided_rows_and_no_optionals(ssd):
     g = _gen("step strided")
     a = _step_inputs(g, 3, 3, 4, 32, 32, 1, 4, torch.bfloat16)
