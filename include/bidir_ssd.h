@@ -421,6 +421,8 @@ ssd_status ssd_conv_bwd(const ssd_conv_shape *shape, const ssd_packed *seq, cons
  * (2^-25).  Decays inside a chunk are differences of float32 sums along it: a
  * term of y is off by a further 2^-22 or so of the chunk's whole decay (as log2),
  * past bf16's rounding only where 128 tokens decay by more than 2^-16384 in all.
+ * Terms of y are carried times up to 2^+-76 there, so they may add up to 2^51 in
+ * absolute values and one below 2^-50 counts as zero.
  * A NaN or an infinity in x, B, C or dt may reach the up to 127 tokens
  * before its own in the same sequence; it never reaches another sequence. */
 typedef struct {

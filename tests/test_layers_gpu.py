@@ -326,6 +326,30 @@ def test_scan_ragged_tensor_core_states_are_float32(ssd, lens, H, direction, bes
         assert float(rms.max()) <= STATE_RMS, (i, rms.max())
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -30, 2.0 ** 44], ids=["small", "large"])
+@pytest.mark.parametrize("direction", [1, -1])
+def test_scan_ragged_tensor_core_range(ssd, direction, scale):
+    """Chunks that decay by just under 2^150, where terms are carried times up to 2^+-76: inputs and states that are
+    that much smaller or larger than one keep their bounds (terms up to 2^51 in all; what is below 2^-50 is lost, 128
+    such terms are 2^-43, here 2^-13 of the smallest sums)."""
+    P, N, H, lens = 64, 128, 4, [300, 77, 128]
+    T, S = sum(lens), len(lens)
+    g = _gen("range", direction)
+    _, x, B, C, _, _, D, _ = _scan_inputs(g, T, H, P, N, 1, torch.bfloat16, False)
+    d = torch.full((T, H), 0.0625).to(torch.bfloat16)
+    A = torch.tensor([-12.9, -12.5, -12.0, -11.0])              # 128 * 0.0625 * 12.9 / ln 2 = 148.9
+    x = (x.float() * scale).to(torch.bfloat16)
+    x, B, C, d, A, D = (v.contiguous().cuda() for v in (x, B, C, d, A, D))
+    pool = (torch.randn(S, H, P, N, generator=g) * scale).cuda()
+    start = [pool[i].clone() for i in range(S)]
+    y = ssd.ssd_scan_ragged(x, d, A, B, C, D, cu_seqlens=_cu(lens), direction=direction, state_in=pool, state_out=pool)
+    ref, ym, last, lastm = ol.scan(x, d, A, B, C, D, lens, None, direction, start)
+    assert float(ym.max()) < 2.0 ** 51
+    _check(y, ref.cpu(), _tc_y(T, N, ref.cpu(), ym.cpu()), "y")
+    for i in range(S):
+        _check(pool[i], last[i].cpu(), _tc_s(T, last[i].cpu(), lastm[i].cpu()), f"state {i}")
+
+
 def test_scan_ragged_repeats_itself(ssd):
     """Equal inputs give equal bits, whatever order the jobs are taken in."""
     g = _gen("repeat scan")
