@@ -69,12 +69,11 @@ template <int EPI, int CG> struct FfnTile {
     static_assert(kSmem <= 232448, "shared memory budget");
 };
 
-// One product of a launch.  a, b: the operands' maps; b2: the second half of B's columns where it is
-// another block of rows (the up projection); d: the outputs' maps (D; or h, gate, up; or gg, gp, h).
+// One product of a launch.  a, b: the operands' maps; d: the outputs' maps (D; or h, gate, up; or gg, gp, h).
 struct FfnProb {
     CUtensorMap a, b, d[3];
     int M, N, K, a_mn, b_mn;
-    int up_row;                    // EPI_GLU: first row of the up projection in W_in
+    int up_row;                    // EPI_GLU: first row of the up projection in W_in (the second half of B's columns)
     int tiles_m, tiles_n, tile0;   // its tiles, and the first one's number in the launch
 };
 struct FfnParams {
@@ -110,13 +109,6 @@ template <int CG> __device__ __forceinline__ void pair_load(uint32_t dst, const 
             "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
             "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
             : "memory");
-}
-// One lane of a converged warp: a stage's four MMAs are issued inside one such branch (each electing its
-// own lane took 4 % longer over the whole block).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t e;
-    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(e));
-    return e != 0;
 }
 template <int CG> __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
     if constexpr (CG == 1) mma_ss(d, a, b, id, acc);
@@ -285,6 +277,7 @@ __global__ void __launch_bounds__(kFfnThreads<EPI>, 1) k_ffn(const __grid_consta
                     tc_fence_after();
                     const uint32_t sa = sbase + st * L::kStage;
                     const SDesc da = make_sdesc(sa, la, 1024), db = make_sdesc(sa + L::kA, lb, 1024);
+                    // (one branch for the stage's four: each electing its own lane took 4 % longer over the block)
                     if (elect_one()) {
 #pragma unroll
                         for (int ks = 0; ks < kFK / 16; ++ks)
@@ -812,13 +805,14 @@ cudaError_t launch_ffn(const FfnArgs &a, cudaStream_t st) {
         ok = ok && map_of(&q.d[1], a.gu, a.T, a.F, 2ull * a.F, 32) &&
              map_of(&q.d[2], static_cast<__nv_bfloat16 *>(a.gu) + a.F, a.T, a.F, 2ull * a.F, 32);
     if (!ok) return cudaErrorInvalidValue;
-    cudaError_t e = run_ffn_any<EPI_GLU>(prm, st);
+    static_assert(kFewMax >= 128, "more tokens than a single CTA's rows: pairs");
+    cudaError_t e = run_ffn<EPI_GLU, 2>(prm, st);
     if (e != cudaSuccess) return e;
     prm.wait_prior = 1;
     q = product(a.T, a.D, a.F, false, false);
     if (!operand(&q.a, a.h, a.T, a.F, false) || !operand(&q.b, a.W_out, a.D, a.F, false) || !map_of(&q.d[0], a.out, a.T, a.D, a.D, 32))
         return cudaErrorInvalidValue;
-    return run_ffn_any<EPI_PLAIN>(prm, st);
+    return run_ffn<EPI_PLAIN, 2>(prm, st);
 }
 
 cudaError_t launch_ffn_bwd(const FfnArgs &a, cudaStream_t st) {

@@ -13,8 +13,7 @@ namespace ssd {
 
 // Codes that the kernels on packed batches write into the status word when an index array does not
 // hold what the call's contract says; the work concerned is skipped, nothing is read or written
-// outside the buffers.  (Codes below kArgCode are waits that gave up.)
-constexpr int kArgCode = 1000;
+// outside the buffers.  (Smaller codes are waits that gave up.)
 constexpr int kCodeOffsets = 1001;    // cu_seqlens not ascending, or outside the packed rows
 constexpr int kCodeSlotRange = 1002;  // a slot index past the pool
 constexpr int kCodeSlotTwice = 1003;  // a slot that one sequence (or row) writes and another uses
@@ -232,8 +231,6 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
 template <typename T, int V> struct Vec;
 template <> struct Vec<__nv_bfloat16, 4> { using type = uint2; };
 template <> struct Vec<float, 4> { using type = uint4; };
-template <> struct Vec<__nv_bfloat16, 2> { using type = uint32_t; };
-template <> struct Vec<float, 2> { using type = uint2; };
 template <> struct Vec<__nv_bfloat16, 1> { using type = __nv_bfloat16; };
 template <> struct Vec<float, 1> { using type = float; };
 

@@ -98,6 +98,13 @@ __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, long l
     }
 }
 
+// One lane of a converged warp.  A whole run of MMAs is issued inside one such branch.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
 // ------------------------------------------------------------------ fences, TMA
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
