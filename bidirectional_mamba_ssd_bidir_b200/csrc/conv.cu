@@ -12,9 +12,10 @@
 //   gw[K-1-j] = sum_k gs_k x_{k-j},  gb = sum_k gs_k
 //
 // Both passes move each element once.  Measured (bf16, 4352 channels, width 4): forward 16384 tokens 62 us,
-// 4.6 TB/s, 0.71 of the copy rate; backward 16001 tokens 126 us, 3.3 TB/s, 0.51.  Past the bytes it is
-// issue slots that bound them: 15 instructions an element forward and 30 backward, two of them on the
-// quarter-rate unit (ex2, rcp).  Not faster: two channels a thread instead of four, more resident warps
+// 4.6 TB/s, 0.71 of the copy rate; backward 16001 tokens 126 us, 3.3 TB/s, 0.51.  No unit is at its limit: a
+// capture shows issue slots 53 and 49 % busy, ex2 and rcp's unit 56 and 29 %, and most stalls are for fixed
+// latencies.  What is short is warps to hide them, 20 and 12 an SM (96 and 158 registers a thread), and whole
+// waves: 3.2 and 2.6 of them.  Not faster: two channels a thread instead of four, more resident warps
 // with 128 registers (backward 134 us), unpaired multiply-adds (66 and 131 us).
 //
 // A thread owns V = 4 neighbouring channels (1 where the channel count, a stride or an address does

@@ -23,9 +23,12 @@
 // gradient) drain one 256-column TMEM accumulator while the other fills, each warp storing its own 32
 // rows through its own staging boxes.
 // Measured (8177 tokens, d_model 2048, d_ff 8192; bf16 cuBLAS rate 1663 TFLOP/s in a burst, 1390 sustained
-// under the power cap): forward 670 us, 1.23 PFLOP/s; backward 1.62 ms, 1.02 PFLOP/s; on a cool card the
-// projections kernel 404 us, 1.36 PFLOP/s.  The two operands' way from L2 is what is left (10.7 TB/s at
-// 1.4 PFLOP/s): prefetching into L2 ahead of the loads made it 35 % slower, and other orders of the tiles
+// under the power cap): forward 670 to 759 us from card to card, 1.09 to 1.23 PFLOP/s; backward 1.60 to 1.72 ms,
+// 0.96 to 1.03; the projections kernel alone 404 us, 1.36 PFLOP/s, the last launch of the backward pass 1.05.  In
+// captures (1.57 to 1.65 GHz under the cap) the tensor pipe is active 75 % of the projections' time, 62 and 63 %
+// of the two launches of plain products and 47 % of gh with the activation's gradient; L2 gives 44 % of its rate at
+// most, the SM's memory pipes 72 %, so no unit is at its limit, and what the MN-major operands of the backward
+// pass cost is not known.  Prefetching into L2 ahead of the loads made it 35 % slower, other orders of the tiles
 // changed nothing.  Products with few tiles lose to the last wave (256 tiles on 74 pairs: 0.86).
 // An operand may lie along K (K-major: rows of 64 k, the descriptor's usual form) or across it
 // (MN-major: 64 x 64 boxes, 64 rows or columns wide), so nothing is transposed in memory.  Edges of
@@ -476,12 +479,18 @@ __global__ void __launch_bounds__(kFfnThreads<EPI>, 1) k_ffn(const __grid_consta
 //
 // Both forms measured at d_model 2048, d_ff 8192 (us, this one / the other): 3 tokens 26 / 99, 128: 40 /
 // 99, 256: 59 / 88, 512: 69 / 101, 1024: 120 / 126; at 768, 2048: 800 tokens 27 / 36.  Past 1024 tokens the
-// persistent tiles fill the SMs and hide their epilogues.
+// persistent tiles fill the SMs there and hide their epilogues.  The rule goes by tokens alone, not by tiles: with
+// cold caches 256 / 512 / 1024 tokens take 42 / 54 / 52 us at 1024, 4096 (the other form 63 / 54 / 60), 70 / 79 / 126
+// at 2048, 8192 (91 / 101 / 124) and 136 / 227 / 392 at 4096, 16384 (196 / 233 / 331: there it should change
+// over at 512).  Three tokens read the weights at 4.2 and 2.7 TB/s: 128 CTAs in each launch leave 20 SMs without one.
 //
 // gu = [gg gp] W_in of the backward pass has the longest K (2 d_ff) and, with few tokens, next to no tiles: beside
 // the other two products it alone set the time.  Up to 2048 tokens it is a launch of this kernel, W_in
 // taken as it lies (MN-major).  The whole backward pass at d_model 2048, d_ff 8192 (us, so / all three side by
-// side): 16 tokens 81 / 172, 256: 119 / 181, 512: 124 / 196, 1024: 211 / 254, 1500: 310 / 324, 2048: 382 / 391.
+// side): 16 tokens 81 / 172, 256: 119 / 181, 512: 124 / 196, 1024: 211 / 254, 1500: 310 / 324, 2048: 382 / 391; at
+// 4096, 16384 with cold caches 256: 259 / 413, 1024: 734 / 788, 2048: 1492 / 1607, at 1024, 4096 2048: 136 / 157.
+// What is left of few tokens or small widths is gh in its large tiles: 333 tokens at 488, 1160 put it on 20 SMs, 31
+// of the three launches' 59 us with cold caches.
 constexpr int kFewMax = 1024, kFewGrad = 2048;
 template <int N> struct FewTile {
     static constexpr uint32_t kW = 128 * 128, kU = N * 128, kStage = kW + kU;

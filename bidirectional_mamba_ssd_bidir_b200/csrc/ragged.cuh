@@ -306,8 +306,8 @@ template <int V> __device__ __forceinline__ void add_v(const float (&a)[V], cons
     }
 }
 
-// sigma[i] = 1 / (1 + e^-v[i]), each from one ex2 and one rcp (approximations within 2 ulp; results
-// below 2^-126 flush to zero).  e^-v past the float range makes it 0, as it should be.
+// sigma[i] = 1 / (1 + e^-v[i]), each from one ex2 and one rcp (approximations within 2 ulp, and the rounded
+// argument of ex2 adds up to |v| ulp; results below 2^-126 flush to zero).  e^-v past the float range makes it 0, as it should be.
 template <int V> __device__ __forceinline__ void sigmoids(const float (&v)[V], float (&sg)[V]) {
     float c[V], e[V];
 #pragma unroll

@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_ragged_tc(const __grid_consta
 // that the next half is weighed while they run: 16 warps weigh, two buffers of w x, three stages of x and
 // B, two accumulators; a chunk's sum is added to S while the next chunk's first half is multiplied.
 // A segment of this kernel has whole chunks only.  One sequence of 32741 tokens, 64 heads: 135 us with cold
-// caches (2.1 TB/s); the whole call takes 483 us with it, 501 when this was a walk of whole chunks.  x alone
+// caches (2.1 TB/s); on one card the whole call took 483 us with it, 501 when this was a walk of whole chunks.  x alone
 // is 42 us at the HBM rate, the products' operand reads 50; a capture shows the tensor pipe 31 % active,
 // shared memory 35 % and issue slots 45 %, so what is left is the chain load, weigh, multiply of a half.
 constexpr int kHalf = 64, kStThreads = 576;
@@ -863,7 +863,7 @@ struct StMaps {
 // the order of their numbers, and a long job that starts last is waited for by all other SMs.  A chunk
 // counts 2, in the long form 5 (measured 4.4 and 10.5 us).  8 ragged prompts of 16384 tokens in all, 64 heads,
 // 14 % of the chunks long: 291 us, 343 as they are numbered; one
-// sequence of 32741 tokens, whose jobs are alike, 486 either way.
+// sequence of 32741 tokens, whose jobs are alike, the same either way (486 to 524 us from card to card).
 // Sorted by 64 buckets; within one the order is open (results do not depend on it).  One CTA's work, while the
 // others form the states.
 constexpr int kBuckets = 64;

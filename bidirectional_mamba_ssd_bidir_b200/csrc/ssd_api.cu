@@ -856,8 +856,8 @@ ssd_status ragged_plan(const ssd_ragged_shape *s, long long tokens, int nseq, Ra
     if (tokens < 0 || nseq < 0 || tokens + nseq > 0x7fff0000LL) return fail(SSD_ERR_INVALID_ARG, "bad token or sequence count");
     // Tensor-core shapes: one CTA (two heads) to an SM, chunks of 128 tokens, segments for about two CTAs an
     // SM: longer ones leave SMs idle at the end, shorter ones start and fold more states (8 ragged prompts /
-    // one of 32741 tokens, 64 heads, us: one and a half CTAs an SM 274 / 584, two 291 / 486, two and a half
-    // 288 / 571, three 302 / 516, four 320 / 554).
+    // one of 32741 tokens, 64 heads, us on one card: one and a half CTAs an SM 274 / 584, two 291 / 486, two and a
+    // half 288 / 571, three 302 / 516, four 320 / 554).
     // Others: about four CTAs to an SM.
     const bool tc = s->io == SSD_BF16 && s->headdim == 64 && s->dstate == 128 && (s->nheads / s->ngroups) % 2 == 0;
     const long long per_seg = tc ? s->nheads / 2 : s->nheads, quant = tc ? 128 : 32, ctas = tc ? 2 * 148 : 4 * 148;
