@@ -257,6 +257,33 @@ def test_leading_dimensions_out_and_graph(ssd):
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("T", [600, 2300])
+def test_training_step_replays_in_a_graph(ssd, T):
+    """Forward with saved projections and gradients, captured together and replayed on new tokens: both kernels'
+    dependent launches inside a graph."""
+    u, wi, wo, gy = (t.cuda() for t in _inputs(T, 136, 264, 7))
+
+    def run():
+        out, gu = ssd.ffn_block(u, wi, wo, save=True)
+        return [out, gu, *ssd.ffn_block_bwd(u, wi, wo, gu, gy).values()]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for _ in range(3):
+        u.copy_(u.flip(0).clone() * 0.5)
+        gy.copy_(gy.roll(1, 0).clone())
+        graph.replay()
+        want = run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_nan_stays_in_its_token(ssd):
     for T in (40, 300):
         u, wi, wo, _ = _inputs(T, 64, 128)

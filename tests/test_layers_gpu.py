@@ -350,6 +350,46 @@ def test_scan_ragged_tensor_core_range(ssd, direction, scale):
         _check(pool[i], last[i].cpu(), _tc_s(T, last[i].cpu(), lastm[i].cpu()), f"state {i}")
 
 
+@pytest.mark.parametrize("direction", [1, -1])
+def test_rows_before_the_first_sequence(ssd, direction):
+    """cu_seqlens that does not begin at 0: the rows in front, NaN here, are neither used nor written (zero in gx)."""
+    g, lead, tail, lens = _gen("lead", direction), 150, 3, [300, 0, 41]
+    n, T = sum(lens), sum(lens) + lead + tail
+    inner = slice(lead, lead + n)
+    nan = lambda *s: torch.full(s, float("nan"))  # noqa: E731
+
+    def padded(t):
+        return torch.cat([nan(lead, *t.shape[1:]), t.float(), nan(tail, *t.shape[1:])]).to(t.dtype).cuda()
+
+    for dt, C in ((torch.bfloat16, 40), (torch.float32, 13)):
+        x, gy = torch.randn(n, C, generator=g).to(dt), torch.randn(n, C, generator=g).to(dt)
+        w, b = (torch.rand(C, 4, generator=g) - 0.5).cuda(), torch.randn(C, generator=g).cuda()
+        out = torch.full((T, C), 7.0, dtype=dt, device="cuda")
+        ssd.ssd_conv(padded(x), w, b, cu_seqlens=_cu(lens, lead), direction=direction, out=out)
+        assert torch.equal(out[inner], ssd.ssd_conv(x.cuda(), w, b, cu_seqlens=_cu(lens), direction=direction))
+        assert bool((out[:lead] == 7).all()) and bool((out[lead + n:] == 7).all())
+        a = ssd.ssd_conv_bwd(padded(x), w, b, padded(gy), cu_seqlens=_cu(lens, lead), direction=direction)
+        c = ssd.ssd_conv_bwd(x.cuda(), w, b, gy.cuda(), cu_seqlens=_cu(lens), direction=direction)
+        assert torch.equal(a["x"][inner], c["x"]) and bool((a["x"][:lead] == 0).all()) and bool((a["x"][lead + n:] == 0).all())
+        for k in ("w", "bias"):                                 # the runs begin at other rows: another order of n sums
+            assert (a[k] - c[k]).abs().max() <= 4 * n * U * n * 16
+    for dt, H, P, N in ((torch.bfloat16, 2, 64, 128), (torch.float32, 2, 32, 16)):
+        _, x, B, C, d, A, D, _ = _scan_inputs(g, n, H, P, N, 1, dt, False)
+        out = torch.full((T, H, P), 7.0, dtype=dt, device="cuda")
+        state = torch.empty(3, H, P, N, device="cuda")
+        ssd.ssd_scan_ragged(*(padded(t) for t in (x, d)), A.cuda(), *(padded(t) for t in (B, C)), D.cuda(), cu_seqlens=_cu(lens, lead),
+                            direction=direction, state_out=state, out=out)
+        ref, ym, last, lastm = ol.scan(x, d, A, B, C, D, lens, None, direction)
+        assert bool((out[:lead] == 7).all()) and bool((out[lead + n:] == 7).all())
+        if dt is torch.bfloat16:
+            ty, ts = _tc_y(300, N, ref, ym), _tc_s
+        else:
+            ty, ts = (HALF[dt] * ref.abs() + (6 * 300 + 2 * N + 41) * U * ym + 1e-37), lambda k, s, m: (6 * 300 + 40) * U * m + 1e-37  # noqa: E731
+        _check(out[inner], ref, ty, "y")
+        for i in range(3):
+            _check(state[i], last[i], ts(300, last[i], lastm[i]), f"state {i}")
+
+
 def test_scan_ragged_repeats_itself(ssd):
     """Equal inputs give equal bits, whatever order the jobs are taken in."""
     g = _gen("repeat scan")
