@@ -863,7 +863,7 @@ struct StMaps {
 // the order of their numbers, and a long job that starts last is waited for by all other SMs.  A chunk
 // counts 2, in the long form 5 (measured 4.4 and 10.5 us).  8 ragged prompts of 16384 tokens in all, 64 heads,
 // 14 % of the chunks long: 291 us, 343 as they are numbered; one
-// sequence of 32741 tokens, whose jobs are alike, the same either way (486 to 524 us from card to card).
+// sequence of 32741 tokens, whose jobs are alike, the same either way (486 to 531 us from run to run).
 // Sorted by 64 buckets; within one the order is open (results do not depend on it).  One CTA's work, while the
 // others form the states.
 constexpr int kBuckets = 64;
